@@ -135,7 +135,8 @@ def _quantise(u):
     """Codes and scales of the rows of u (fp32): scale = max|row| / 127 in fp32,
     code = u / scale rounded half to even. The quotient is taken in 64 bits, so
     that a value next to a border falls on its own side of it."""
-    s = u.abs().amax(1) / 127
+    top = u.abs().amax(1)
+    s = top / torch.full_like(top, 127.0)  # by a tensor: torch turns a division by a number into a product
     q = torch.round(u.double() / s.double()[:, None]).clamp(-127, 127)
     return torch.where(s[:, None] > 0, q, 0.0).float(), s
 
@@ -249,7 +250,8 @@ def work(case):
 # ---------------------------------------------------------------- in 64 bits
 def _codes64(u):
     """Rows of fp32 values -> (codes, scales) as fp64, from the quantiser's definition."""
-    s = (u.abs().max(dim=1).values / 127).double()
+    top = u.abs().max(dim=1).values
+    s = top.div(torch.full_like(top, 127.0)).double()
     live = s > 0
     q = u.double().div(torch.where(live, s, 1.0).unsqueeze(1)).round()
     return q.clamp(-127.0, 127.0) * live.unsqueeze(1), s
