@@ -269,6 +269,86 @@ poetx_status poetx_weight_quantize(int32_t n, int32_t m, const void* W, int32_t 
 poetx_status poetx_weight_dequantize(int32_t n, int32_t m, const int8_t* Wq, const float* scale, int32_t dtype,
                                      void* W, void* stream);
 
+/* ---------------------------------------------------------------- 8-bit path
+ * Operators around the int8 weight of POET-XQ (no counterpart in the
+ * write-up).  Rows are contiguous, 1 <= d, n, m <= 102400 (51200 for the
+ * norm), T = 0 is a no-op except where said otherwise.  Outputs may not
+ * overlap inputs or each other unless a call says so.
+ *
+ * Quantised rows: scale = max|row| / 127 (fp32 division), code = row / scale
+ * rounded half to even (the real quotient, not a rounded one).  A row of
+ * zeros gets scale 0; a row that holds an infinity or a NaN gets codes 0 and
+ * scale NaN.
+ *
+ * poetx_quantize_rows: x [T][d] (dtype) -> xq [T][d] int8, xscale [T] fp32.
+ * With colscale ([d] fp32, nullable) the rows are x * colscale, each product
+ * rounded to fp32. */
+poetx_status poetx_quantize_rows(int64_t T, int32_t d, const void* x, int32_t dtype, const float* colscale,
+                                 int8_t* xq, float* xscale, void* stream);
+
+/* Root-mean-square norm with the residual's addition and quantised rows:
+ *   h    = x + residual, rounded once to dtype (residual NULL: h = x)
+ *   rstd = 1 / sqrt(mean(h^2) + eps)           (fp32, finite eps > 0)
+ *   u    = h * gamma                            (gamma [d] fp32)
+ *   xq, xscale: u quantised as above, the scale times rstd
+ *   y    = u * rstd rounded to dtype
+ * x, residual, h, y [T][d] (dtype); rstd [T].  Needed: x, gamma, at least one
+ * of xq and y (xq and xscale together), and h with a residual; the rest may be
+ * NULL.  h may be x or residual, y may be x where h is NULL. */
+poetx_status poetx_rmsnorm_quantize(int64_t T, int32_t d, const void* x, const void* residual, const float* gamma,
+                                    float eps, int32_t dtype, void* h, void* y, int8_t* xq, float* xscale,
+                                    float* rstd, void* stream);
+
+/* Backward of the norm (the quantiser passes gradients through): from dy
+ * [T][d], the forward's h and rstd, and dres [T][d] (nullable; the gradient
+ * that reaches h past the norm), with p = dy * gamma:
+ *   dx = rstd (p - h rstd^2 mean(p h)) + dres   (dtype; of x and of residual)
+ *   dgamma [d] (fp32) = sum over tokens of dy h rstd, overwritten, or added to
+ *   when accumulate != 0; the sum's order depends on (T, d) alone.
+ * T = 0 clears dgamma unless accumulate is set.  dx may be dy, h or dres. */
+size_t poetx_rmsnorm_backward_workspace_bytes(int64_t T, int32_t d);
+poetx_status poetx_rmsnorm_backward(int64_t T, int32_t d, const void* dy, const void* h, const float* gamma,
+                                    const float* rstd, const void* dres, int32_t dtype, void* dx, float* dgamma,
+                                    int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/* Int8 product with a scale per token and per channel:
+ *   out[t][j] = xscale[t] wscale[j] sum_i xq[t][i] Wq[j][i]
+ * xq [T][m], Wq [n][m] int8 (any codes), xscale [T], wscale [n] fp32, out
+ * [T][n] (dtype).  The sum is exact (32-bit integers); the scales are applied
+ * in fp32, xscale first. */
+poetx_status poetx_matmul_int8(int64_t T, int32_t n, int32_t m, const int8_t* xq, const float* xscale,
+                               const int8_t* Wq, const float* wscale, int32_t dtype, void* out, void* stream);
+
+/* Gradient of that product with respect to its tokens, in 8 bits too: the
+ * rows of dz * wscale ([T][n], each product rounded to fp32) are quantised as
+ * above to (gq, gs), and dx[t][i] = gs[t] sum_j gq[t][j] Wq[j][i] (dtype). */
+size_t poetx_matmul_int8_grad_workspace_bytes(int64_t T, int32_t n, int32_t m);
+poetx_status poetx_matmul_int8_grad(int64_t T, int32_t n, int32_t m, const void* dz, const int8_t* Wq,
+                                    const float* wscale, int32_t dtype, void* dx, void* ws, size_t ws_bytes,
+                                    void* stream);
+
+/* Activation checkpoints in 8 bits: every group of 32 consecutive columns of
+ * a row (the last one may be shorter) shares the exponent e, the smallest with
+ * max|x| <= 127 * 2^e (-126 <= e <= 121; finite values beyond 127 * 2^121 are
+ * kept as that), and x is kept as round-half-even(x / 2^e).  codes [T][d] int8, exps [T][ceil(d / 32)] = e + 127.  A group that
+ * holds an infinity or a NaN gets exps 255 and reads back as NaN.  codes * 2^e
+ * is exact in both dtypes, so load is exact. */
+poetx_status poetx_checkpoint_save(int64_t T, int32_t d, const void* x, int32_t dtype, int8_t* codes, uint8_t* exps,
+                                   void* stream);
+poetx_status poetx_checkpoint_load(int64_t T, int32_t d, const int8_t* codes, const uint8_t* exps, int32_t dtype,
+                                   void* x, void* stream);
+
+/* Backward of one side of a layer (section 1's block products) from the
+ * checkpoint of that side's activation X [T][d], d/b blocks of b columns:
+ *   O_j  = D_j G_j^T    (D, O [T][d], G [d/b][b][b], dtype; O NULL skips it)
+ *   dG_j = X_j^T D_j    (dG [d/b][b][b] fp32, overwritten, or added to when
+ *                        accumulate != 0; a fixed order for a given shape)
+ * b as for a layer of that dtype.  T = 0 clears dG unless accumulate is set. */
+size_t poetx_block_backward_workspace_bytes(int64_t T, int32_t d, int32_t b, int32_t dtype);
+poetx_status poetx_block_backward(int64_t T, int32_t d, int32_t b, const int8_t* codes, const uint8_t* exps,
+                                  const void* D, const void* G, int32_t dtype, void* O, float* dG,
+                                  int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
+
 /* Optimizer step on packed triangles (fp32, n entries): AdamW with decoupled
  * weight decay (the write-up names get_poet_optimizer without describing it;
  * AdamW is the reading taken): m1 <- b1 m1 + (1-b1) g; m2 <- b2 m2 + (1-b2) g^2;
@@ -283,7 +363,8 @@ poetx_status poetx_adamw_step(int64_t n, float* q, const float* grad, float* m1,
  * of CUDA events on its stream and tagged with its stage (permute,
  * blockdiag_gemm, w0_gemm, dg_gemm, cnp_gemm, cnp_elementwise, dg_reduce,
  * merge, dequant, optimizer, blockdiag_dg: the backward's block product and
- * dG partials in one kernel).  poetx_profile_end waits for the recorded events, writes the summed
+ * dG partials in one kernel; quantize, norm, int8_gemm, checkpoint: the 8-bit
+ * path).  poetx_profile_end waits for the recorded events, writes the summed
  * device time in ms (HOST array ms_per_stage[nstages]) and the number of
  * launches (HOST array launches_per_stage[nstages]) per stage, and stops
  * recording.  The events are created on first use and reused. */

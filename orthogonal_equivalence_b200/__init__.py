@@ -74,6 +74,20 @@ SIGNATURES = {
     "poetx_check_perm": (ctypes.c_int, [_VP, _I32, _VP, _VP, _SZ, _VP]),
     "poetx_weight_quantize": (ctypes.c_int, [_I32, _I32, _VP, _I32, _VP, _VP, _VP]),
     "poetx_weight_dequantize": (ctypes.c_int, [_I32, _I32, _VP, _VP, _I32, _VP, _VP]),
+    "poetx_quantize_rows": (ctypes.c_int, [_I64, _I32, _VP, _I32, _VP, _VP, _VP, _VP]),
+    "poetx_rmsnorm_quantize": (ctypes.c_int, [_I64, _I32, _VP, _VP, _VP, ctypes.c_float, _I32, _VP, _VP, _VP, _VP,
+                                              _VP, _VP]),
+    "poetx_rmsnorm_backward_workspace_bytes": (_SZ, [_I64, _I32]),
+    "poetx_rmsnorm_backward": (ctypes.c_int, [_I64, _I32, _VP, _VP, _VP, _VP, _VP, _I32, _VP, _VP, _I32, _VP, _SZ,
+                                              _VP]),
+    "poetx_matmul_int8": (ctypes.c_int, [_I64, _I32, _I32, _VP, _VP, _VP, _VP, _I32, _VP, _VP]),
+    "poetx_matmul_int8_grad_workspace_bytes": (_SZ, [_I64, _I32, _I32]),
+    "poetx_matmul_int8_grad": (ctypes.c_int, [_I64, _I32, _I32, _VP, _VP, _VP, _I32, _VP, _VP, _SZ, _VP]),
+    "poetx_checkpoint_save": (ctypes.c_int, [_I64, _I32, _VP, _I32, _VP, _VP, _VP]),
+    "poetx_checkpoint_load": (ctypes.c_int, [_I64, _I32, _VP, _VP, _I32, _VP, _VP]),
+    "poetx_block_backward_workspace_bytes": (_SZ, [_I64, _I32, _I32, _I32]),
+    "poetx_block_backward": (ctypes.c_int, [_I64, _I32, _I32, _VP, _VP, _VP, _VP, _I32, _VP, _VP, _I32, _VP, _SZ,
+                                            _VP]),
     "poetx_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_uint32, _VP, _VP]),
     "poetx_adamw_step": (ctypes.c_int, [_I64, _VP, _VP, _VP, _VP, ctypes.c_float, ctypes.c_float, ctypes.c_float,
                                         ctypes.c_float, ctypes.c_float, _I32, _VP]),
@@ -255,6 +269,64 @@ def poetx_weight_dequantize(n: int, m: int, Wq, scale, dtype: int, W, stream=Non
            "poetx_weight_dequantize")
 
 
+def poetx_quantize_rows(T: int, d: int, x, dtype: int, colscale, xq, xscale, stream=None) -> None:
+    _check(lib().poetx_quantize_rows(T, d, _ptr(x), dtype, _ptr(colscale), _ptr(xq), _ptr(xscale), _stream(stream)),
+           "poetx_quantize_rows")
+
+
+def poetx_rmsnorm_quantize(T: int, d: int, x, residual, gamma, eps: float, dtype: int, h, y, xq, xscale, rstd,
+                           stream=None) -> None:
+    _check(lib().poetx_rmsnorm_quantize(T, d, _ptr(x), _ptr(residual), _ptr(gamma), eps, dtype, _ptr(h), _ptr(y),
+                                        _ptr(xq), _ptr(xscale), _ptr(rstd), _stream(stream)),
+           "poetx_rmsnorm_quantize")
+
+
+def poetx_rmsnorm_backward_workspace_bytes(T: int, d: int) -> int:
+    return lib().poetx_rmsnorm_backward_workspace_bytes(T, d)
+
+
+def poetx_rmsnorm_backward(T: int, d: int, dy, h, gamma, rstd, dres, dtype: int, dx, dgamma, accumulate: int, ws,
+                           ws_bytes: int, stream=None) -> None:
+    _check(lib().poetx_rmsnorm_backward(T, d, _ptr(dy), _ptr(h), _ptr(gamma), _ptr(rstd), _ptr(dres), dtype, _ptr(dx),
+                                        _ptr(dgamma), accumulate, _ptr(ws), ws_bytes, _stream(stream)),
+           "poetx_rmsnorm_backward")
+
+
+def poetx_matmul_int8(T: int, n: int, m: int, xq, xscale, Wq, wscale, dtype: int, out, stream=None) -> None:
+    _check(lib().poetx_matmul_int8(T, n, m, _ptr(xq), _ptr(xscale), _ptr(Wq), _ptr(wscale), dtype, _ptr(out),
+                                   _stream(stream)), "poetx_matmul_int8")
+
+
+def poetx_matmul_int8_grad_workspace_bytes(T: int, n: int, m: int) -> int:
+    return lib().poetx_matmul_int8_grad_workspace_bytes(T, n, m)
+
+
+def poetx_matmul_int8_grad(T: int, n: int, m: int, dz, Wq, wscale, dtype: int, dx, ws, ws_bytes: int,
+                           stream=None) -> None:
+    _check(lib().poetx_matmul_int8_grad(T, n, m, _ptr(dz), _ptr(Wq), _ptr(wscale), dtype, _ptr(dx), _ptr(ws),
+                                        ws_bytes, _stream(stream)), "poetx_matmul_int8_grad")
+
+
+def poetx_checkpoint_save(T: int, d: int, x, dtype: int, codes, exps, stream=None) -> None:
+    _check(lib().poetx_checkpoint_save(T, d, _ptr(x), dtype, _ptr(codes), _ptr(exps), _stream(stream)),
+           "poetx_checkpoint_save")
+
+
+def poetx_checkpoint_load(T: int, d: int, codes, exps, dtype: int, x, stream=None) -> None:
+    _check(lib().poetx_checkpoint_load(T, d, _ptr(codes), _ptr(exps), dtype, _ptr(x), _stream(stream)),
+           "poetx_checkpoint_load")
+
+
+def poetx_block_backward_workspace_bytes(T: int, d: int, b: int, dtype: int) -> int:
+    return lib().poetx_block_backward_workspace_bytes(T, d, b, dtype)
+
+
+def poetx_block_backward(T: int, d: int, b: int, codes, exps, D, G, dtype: int, O, dG, accumulate: int, ws,
+                         ws_bytes: int, stream=None) -> None:
+    _check(lib().poetx_block_backward(T, d, b, _ptr(codes), _ptr(exps), _ptr(D), _ptr(G), dtype, _ptr(O), _ptr(dG),
+                                      accumulate, _ptr(ws), ws_bytes, _stream(stream)), "poetx_block_backward")
+
+
 def poetx_adamw_step(n: int, q, grad, m1, m2, lr: float, beta1: float, beta2: float, eps: float,
                      weight_decay: float, step: int, stream=None) -> None:
     _check(lib().poetx_adamw_step(n, _ptr(q), _ptr(grad), _ptr(m1), _ptr(m2), lr, beta1, beta2, eps, weight_decay,
@@ -292,3 +364,6 @@ def poetx_profile_records() -> list:
 
 
 from .layer import LayerGroup, PoetxLinear, Saved  # noqa: E402,F401
+from .quantized import (Checkpoint, NormRows, QuantRows, block_backward, checkpoint_load, checkpoint_save,  # noqa: E402,F401
+                        dequantize_rows, matmul_int8, matmul_int8_grad, quantize_rows, rmsnorm_backward,
+                        rmsnorm_quantize)

@@ -22,6 +22,8 @@
 #include "cnp2sm.cuh"
 #include "cnp2build.cuh"
 #include "bdg2sm.cuh"
+#include "q8.cuh"
+#include "gemm_i8.cuh"
 
 using namespace poetx;
 
@@ -139,11 +141,15 @@ enum Stage : int {
   ST_DEQUANT,
   ST_OPTIM,
   ST_BDG,
+  ST_QUANT,
+  ST_NORM,
+  ST_INT8,
+  ST_CKPT,
   ST_COUNT
 };
 const char* const kStageNames[ST_COUNT] = {"permute",  "blockdiag_gemm",  "w0_gemm",   "dg_gemm", "cnp_gemm",
                                            "cnp_elementwise", "dg_reduce", "merge", "dequant", "optimizer",
-                                            "blockdiag_dg"};
+                                            "blockdiag_dg", "quantize", "norm", "int8_gemm", "checkpoint"};
 
 struct Profiler {
   std::mutex mu;
@@ -1766,3 +1772,387 @@ extern "C" poetx_status poetx_adamw_step(int64_t n, float* q, const float* grad,
   POETX_CUDA(cudaGetLastError());
   return POETX_OK;
 }
+
+// ======================================================================== 8-bit path
+namespace {
+
+constexpr int32_t kMaxD8 = 102400;  // widest row: |code| <= 128 keeps a sum of that many products below 2^31
+
+poetx_status check_dtype(int32_t dtype) {
+  return dtype == POETX_FP32 || dtype == POETX_BF16 ? POETX_OK : POETX_E_DTYPE;
+}
+
+poetx_status check_rows(int64_t T, int32_t d, int32_t max_d) {
+  if (T < 0 || d <= 0) return POETX_E_ARG;
+  return T > kMaxT || d > max_d ? POETX_E_SHAPE : POETX_OK;
+}
+
+poetx_status check_opt(const void* p) { return aligned16(p) ? POETX_OK : POETX_E_ALIGN; }
+
+// Threads and registers of a row: V = 8 elements a load where the row length
+// allows (16-byte rows), E elements a thread, at most 512 threads; wider rows
+// (E = 0) are read twice.
+struct RowShape {
+  int V, E, threads;
+};
+RowShape row_shape(int d) {
+  RowShape r;
+  r.V = d % 8 == 0 ? 8 : 1;
+  r.E = d <= 8 * 512 ? 8 : d <= 16 * 512 ? 16 : d <= 32 * 512 ? 32 : 0;
+  const int per = r.E ? r.E : 32;
+  const int t = ((d + per - 1) / per + 31) / 32 * 32;
+  r.threads = t < 512 ? t : 512;
+  return r;
+}
+
+int row_grid(int64_t T, int threads, int device) {
+  const int64_t g = int64_t(sm_count(device)) * (2048 / threads);
+  return static_cast<int>(T < g ? T : g);
+}
+
+template <typename T, bool NORM>
+cudaError_t launch_rows(const q8::RowsParams& p, cudaStream_t st, int device) {
+  const RowShape r = row_shape(p.d);
+  const int grid = row_grid(p.T, r.threads, device);
+  if (r.V == 8) {
+    if (r.E == 8) q8::rows_kernel<T, NORM, 8, 1><<<grid, r.threads, 0, st>>>(p);
+    else if (r.E == 16) q8::rows_kernel<T, NORM, 8, 2><<<grid, r.threads, 0, st>>>(p);
+    else if (r.E == 32) q8::rows_kernel<T, NORM, 8, 4><<<grid, r.threads, 0, st>>>(p);
+    else q8::rows_kernel<T, NORM, 8, 0><<<grid, r.threads, 0, st>>>(p);
+  } else {
+    if (r.E == 8) q8::rows_kernel<T, NORM, 1, 8><<<grid, r.threads, 0, st>>>(p);
+    else if (r.E == 16) q8::rows_kernel<T, NORM, 1, 16><<<grid, r.threads, 0, st>>>(p);
+    else if (r.E == 32) q8::rows_kernel<T, NORM, 1, 32><<<grid, r.threads, 0, st>>>(p);
+    else q8::rows_kernel<T, NORM, 1, 0><<<grid, r.threads, 0, st>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+template <bool NORM>
+cudaError_t launch_rows_dt(int32_t dtype, const q8::RowsParams& p, cudaStream_t st, int device) {
+  return dtype == POETX_BF16 ? launch_rows<__nv_bfloat16, NORM>(p, st, device)
+                             : launch_rows<float, NORM>(p, st, device);
+}
+
+cudaError_t quantize_rows(int64_t T, int32_t d, const void* x, int32_t dtype, const float* colscale, int8_t* codes,
+                          int64_t ldc, float* scale, cudaStream_t st, int device) {
+  q8::RowsParams p{};
+  p.x = x;
+  p.gain = colscale;
+  p.codes = codes;
+  p.ldc = ldc;
+  p.scale = scale;
+  p.T = T;
+  p.d = d;
+  PROFILED(ST_QUANT, st, POETX_CUDA_ERR(launch_rows_dt<false>(dtype, p, st, device)));
+  return cudaSuccess;
+}
+
+// Blocks of the norm's backward: a fixed number, so that the sums of dgamma
+// do not depend on the device.
+int norm_grad_grid(int64_t T, int threads) {
+  const int64_t g = int64_t(kSplitSMs) * (1024 / threads < 1 ? 1 : 1024 / threads);
+  return static_cast<int>(T < g ? T : g);
+}
+
+template <typename T, int V, int K>
+cudaError_t launch_norm_grad_k(const q8::NormGradParams& p, int grid, int threads, cudaStream_t st, int device) {
+  const size_t smem = K > 0 ? 0 : sizeof(float) * size_t(p.d);
+  static bool attr[64] = {false};
+  cudaError_t e = allow_smem(q8::norm_grad_kernel<T, V, K>, smem, &attr[device & 63]);
+  if (e != cudaSuccess) return e;
+  q8::norm_grad_kernel<T, V, K><<<grid, threads, smem, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_norm_grad(const q8::NormGradParams& p, int grid, const RowShape& r, cudaStream_t st, int device) {
+  if (r.V == 8) {
+    if (r.E == 8) return launch_norm_grad_k<T, 8, 1>(p, grid, r.threads, st, device);
+    if (r.E == 16) return launch_norm_grad_k<T, 8, 2>(p, grid, r.threads, st, device);
+    if (r.E == 32) return launch_norm_grad_k<T, 8, 4>(p, grid, r.threads, st, device);
+    return launch_norm_grad_k<T, 8, 0>(p, grid, r.threads, st, device);
+  }
+  if (r.E == 8) return launch_norm_grad_k<T, 1, 8>(p, grid, r.threads, st, device);
+  if (r.E == 16) return launch_norm_grad_k<T, 1, 16>(p, grid, r.threads, st, device);
+  if (r.E == 32) return launch_norm_grad_k<T, 1, 32>(p, grid, r.threads, st, device);
+  return launch_norm_grad_k<T, 1, 0>(p, grid, r.threads, st, device);
+}
+
+template <typename T>
+cudaError_t launch_checkpoint(bool save, const void* src, int8_t* codes, uint8_t* exps, void* dst, int64_t T_, int d,
+                              cudaStream_t st, int device) {
+  const int V = d % 8 == 0 ? 8 : 1;
+  const int64_t warps = T_ * ((d + 32 * V - 1) / (32 * V));
+  int64_t grid = (warps + 7) / 8;
+  const int64_t cap = int64_t(sm_count(device)) * 8;
+  if (grid > cap) grid = cap;
+  const int g = static_cast<int>(grid);
+  if (save) {
+    if (V == 8) q8::checkpoint_save_kernel<T, 8><<<g, 256, 0, st>>>(static_cast<const T*>(src), T_, d, codes, exps);
+    else q8::checkpoint_save_kernel<T, 1><<<g, 256, 0, st>>>(static_cast<const T*>(src), T_, d, codes, exps);
+  } else {
+    if (V == 8) q8::checkpoint_load_kernel<T, 8><<<g, 256, 0, st>>>(codes, exps, T_, d, static_cast<T*>(dst));
+    else q8::checkpoint_load_kernel<T, 1><<<g, 256, 0, st>>>(codes, exps, T_, d, static_cast<T*>(dst));
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t checkpoint_save(int64_t T, int32_t d, const void* x, int32_t dtype, int8_t* codes, uint8_t* exps,
+                            cudaStream_t st, int device) {
+  PROFILED(ST_CKPT, st,
+           POETX_CUDA_ERR(dtype == POETX_BF16
+                              ? launch_checkpoint<__nv_bfloat16>(true, x, codes, exps, nullptr, T, d, st, device)
+                              : launch_checkpoint<float>(true, x, codes, exps, nullptr, T, d, st, device)));
+  return cudaSuccess;
+}
+
+cudaError_t checkpoint_load(int64_t T, int32_t d, const int8_t* codes, const uint8_t* exps, int32_t dtype, void* x,
+                            cudaStream_t st, int device) {
+  int8_t* c = const_cast<int8_t*>(codes);
+  uint8_t* e = const_cast<uint8_t*>(exps);
+  PROFILED(ST_CKPT, st,
+           POETX_CUDA_ERR(dtype == POETX_BF16 ? launch_checkpoint<__nv_bfloat16>(false, nullptr, c, e, x, T, d, st, device)
+                                              : launch_checkpoint<float>(false, nullptr, c, e, x, T, d, st, device)));
+  return cudaSuccess;
+}
+
+cudaError_t product_i8(const i8::Params& p, bool b_kn, int32_t dtype, cudaStream_t st) {
+  const dim3 grid((p.M + i8::TILE - 1) / i8::TILE, (p.N + i8::TILE - 1) / i8::TILE);
+  Prof prof(ST_INT8, st);
+  if (dtype == POETX_BF16) {
+    if (b_kn) i8::product_kernel<__nv_bfloat16, true><<<grid, 256, 0, st>>>(p);
+    else i8::product_kernel<__nv_bfloat16, false><<<grid, 256, 0, st>>>(p);
+  } else {
+    if (b_kn) i8::product_kernel<float, true><<<grid, 256, 0, st>>>(p);
+    else i8::product_kernel<float, false><<<grid, 256, 0, st>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+size_t grad_i8_ws(int64_t T, int32_t n) { return kAlign + al(size_t(T) * n) + al(sizeof(float) * size_t(T)); }
+
+size_t block_backward_ws(int64_t T, int32_t d, int32_t b, int32_t dtype) {
+  return kAlign + al(size_t(dtype_size(dtype)) * T * d) +
+         al(sizeof(float) * size_t(dg_splits(d / b, b, T, dtype)) * d * b);
+}
+
+poetx_status check_block(int64_t T, int32_t d, int32_t b, int32_t dtype) {
+  POETX_TRY(check_dtype_b(dtype, b));
+  POETX_TRY(check_rows(T, d, kMaxD8));
+  return d % b == 0 ? POETX_OK : POETX_E_SHAPE;
+}
+
+}  // namespace
+
+extern "C" {
+
+poetx_status poetx_quantize_rows(int64_t T, int32_t d, const void* x, int32_t dtype, const float* colscale,
+                                 int8_t* xq, float* xscale, void* stream) {
+  POETX_TRY(check_dtype(dtype));
+  POETX_TRY(check_rows(T, d, kMaxD8));
+  if (T == 0) return POETX_OK;
+  POETX_TRY(check_ptr(x));
+  POETX_TRY(check_opt(colscale));
+  POETX_TRY(check_ptr(xq));
+  POETX_TRY(check_ptr(xscale));
+  int dev;
+  POETX_TRY(current_device(&dev));
+  POETX_CUDA(quantize_rows(T, d, x, dtype, colscale, xq, d, xscale, static_cast<cudaStream_t>(stream), dev));
+  return POETX_OK;
+}
+
+poetx_status poetx_rmsnorm_quantize(int64_t T, int32_t d, const void* x, const void* residual, const float* gamma,
+                                    float eps, int32_t dtype, void* h, void* y, int8_t* xq, float* xscale,
+                                    float* rstd, void* stream) {
+  POETX_TRY(check_dtype(dtype));
+  POETX_TRY(check_rows(T, d, kMaxM));
+  if (!(eps > 0.f) || !(eps < 3e38f)) return POETX_E_ARG;
+  if (T == 0) return POETX_OK;
+  if ((!xq && !y) || (!xq) != (!xscale) || (residual && !h)) return POETX_E_ARG;
+  POETX_TRY(check_ptr(x));
+  POETX_TRY(check_ptr(gamma));
+  const void* opt[] = {residual, h, y, xq, xscale, rstd};
+  for (const void* p : opt) POETX_TRY(check_opt(p));
+  int dev;
+  POETX_TRY(current_device(&dev));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  q8::RowsParams p{};
+  p.x = x;
+  p.residual = residual;
+  p.gain = gamma;
+  p.h = h;
+  p.y = y;
+  p.codes = xq;
+  p.ldc = d;
+  p.scale = xscale;
+  p.rstd = rstd;
+  p.T = T;
+  p.d = d;
+  p.eps = eps;
+  PROFILED(ST_NORM, st, POETX_CUDA(launch_rows_dt<true>(dtype, p, st, dev)));
+  return POETX_OK;
+}
+
+size_t poetx_rmsnorm_backward_workspace_bytes(int64_t T, int32_t d) {
+  if (check_rows(T, d, kMaxM) != POETX_OK) return 0;
+  return kAlign + al(sizeof(float) * size_t(norm_grad_grid(T, row_shape(d).threads)) * d);
+}
+
+poetx_status poetx_rmsnorm_backward(int64_t T, int32_t d, const void* dy, const void* h, const float* gamma,
+                                    const float* rstd, const void* dres, int32_t dtype, void* dx, float* dgamma,
+                                    int32_t accumulate, void* ws, size_t ws_bytes, void* stream) {
+  POETX_TRY(check_dtype(dtype));
+  POETX_TRY(check_rows(T, d, kMaxM));
+  POETX_TRY(check_ptr(dgamma));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (T == 0) {
+    if (!accumulate) POETX_CUDA(cudaMemsetAsync(dgamma, 0, sizeof(float) * size_t(d), st));
+    return POETX_OK;
+  }
+  const void* need[] = {dy, h, gamma, rstd, dx};
+  for (const void* p : need) POETX_TRY(check_ptr(p));
+  POETX_TRY(check_opt(dres));
+  if (!ws || ws_bytes < poetx_rmsnorm_backward_workspace_bytes(T, d)) return POETX_E_WORKSPACE;
+  int dev;
+  POETX_TRY(current_device(&dev));
+  const RowShape r = row_shape(d);
+  const int grid = norm_grad_grid(T, r.threads);
+  Carver c(ws, ws_bytes);
+  q8::NormGradParams p;
+  p.dy = dy;
+  p.h = h;
+  p.gamma = gamma;
+  p.rstd = rstd;
+  p.dres = dres;
+  p.dx = dx;
+  p.part = c.take<float>(sizeof(float) * size_t(grid) * d);
+  p.T = T;
+  p.d = d;
+  PROFILED(ST_NORM, st,
+           POETX_CUDA(dtype == POETX_BF16 ? launch_norm_grad<__nv_bfloat16>(p, grid, r, st, dev)
+                                          : launch_norm_grad<float>(p, grid, r, st, dev)));
+  PROFILED(ST_NORM, st,
+           q8::sum_partials_kernel<<<(d + 31) / 32, 256, 0, st>>>(p.part, grid, d, dgamma, accumulate));
+  POETX_CUDA(cudaGetLastError());
+  return POETX_OK;
+}
+
+poetx_status poetx_matmul_int8(int64_t T, int32_t n, int32_t m, const int8_t* xq, const float* xscale,
+                               const int8_t* Wq, const float* wscale, int32_t dtype, void* out, void* stream) {
+  POETX_TRY(check_dtype(dtype));
+  POETX_TRY(check_rows(T, m, kMaxD8));
+  POETX_TRY(check_rows(T, n, kMaxD8));
+  if (T == 0) return POETX_OK;
+  const void* need[] = {xq, xscale, Wq, wscale, out};
+  for (const void* p : need) POETX_TRY(check_ptr(p));
+  int dev;
+  POETX_TRY(current_device(&dev));
+  i8::Params p{xq, Wq, xscale, wscale, out, m, m, static_cast<int>(T), n, m};
+  POETX_CUDA(product_i8(p, false, dtype, static_cast<cudaStream_t>(stream)));
+  return POETX_OK;
+}
+
+size_t poetx_matmul_int8_grad_workspace_bytes(int64_t T, int32_t n, int32_t m) {
+  if (check_rows(T, n, kMaxD8) != POETX_OK || check_rows(T, m, kMaxD8) != POETX_OK) return 0;
+  return grad_i8_ws(T, n);
+}
+
+poetx_status poetx_matmul_int8_grad(int64_t T, int32_t n, int32_t m, const void* dz, const int8_t* Wq,
+                                    const float* wscale, int32_t dtype, void* dx, void* ws, size_t ws_bytes,
+                                    void* stream) {
+  POETX_TRY(check_dtype(dtype));
+  POETX_TRY(check_rows(T, m, kMaxD8));
+  POETX_TRY(check_rows(T, n, kMaxD8));
+  if (T == 0) return POETX_OK;
+  const void* need[] = {dz, Wq, wscale, dx};
+  for (const void* p : need) POETX_TRY(check_ptr(p));
+  if (!ws || ws_bytes < grad_i8_ws(T, n)) return POETX_E_WORKSPACE;
+  int dev;
+  POETX_TRY(current_device(&dev));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Carver c(ws, ws_bytes);
+  int8_t* gq = c.take<int8_t>(size_t(T) * n);
+  float* gs = c.take<float>(sizeof(float) * size_t(T));
+  POETX_CUDA(quantize_rows(T, n, dz, dtype, wscale, gq, n, gs, st, dev));
+  i8::Params p{gq, Wq, gs, nullptr, dx, n, m, static_cast<int>(T), m, n};
+  POETX_CUDA(product_i8(p, true, dtype, st));
+  return POETX_OK;
+}
+
+poetx_status poetx_checkpoint_save(int64_t T, int32_t d, const void* x, int32_t dtype, int8_t* codes, uint8_t* exps,
+                                   void* stream) {
+  POETX_TRY(check_dtype(dtype));
+  POETX_TRY(check_rows(T, d, kMaxD8));
+  if (T == 0) return POETX_OK;
+  POETX_TRY(check_ptr(x));
+  POETX_TRY(check_ptr(codes));
+  POETX_TRY(check_ptr(exps));
+  int dev;
+  POETX_TRY(current_device(&dev));
+  POETX_CUDA(checkpoint_save(T, d, x, dtype, codes, exps, static_cast<cudaStream_t>(stream), dev));
+  return POETX_OK;
+}
+
+poetx_status poetx_checkpoint_load(int64_t T, int32_t d, const int8_t* codes, const uint8_t* exps, int32_t dtype,
+                                   void* x, void* stream) {
+  POETX_TRY(check_dtype(dtype));
+  POETX_TRY(check_rows(T, d, kMaxD8));
+  if (T == 0) return POETX_OK;
+  POETX_TRY(check_ptr(x));
+  POETX_TRY(check_ptr(codes));
+  POETX_TRY(check_ptr(exps));
+  int dev;
+  POETX_TRY(current_device(&dev));
+  POETX_CUDA(checkpoint_load(T, d, codes, exps, dtype, x, static_cast<cudaStream_t>(stream), dev));
+  return POETX_OK;
+}
+
+size_t poetx_block_backward_workspace_bytes(int64_t T, int32_t d, int32_t b, int32_t dtype) {
+  if (check_block(T, d, b, dtype) != POETX_OK) return 0;
+  return block_backward_ws(T, d, b, dtype);
+}
+
+poetx_status poetx_block_backward(int64_t T, int32_t d, int32_t b, const int8_t* codes, const uint8_t* exps,
+                                  const void* D, const void* G, int32_t dtype, void* O, float* dG,
+                                  int32_t accumulate, void* ws, size_t ws_bytes, void* stream) {
+  POETX_TRY(check_block(T, d, b, dtype));
+  POETX_TRY(check_ptr(dG));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (T == 0) {
+    if (!accumulate) POETX_CUDA(cudaMemsetAsync(dG, 0, sizeof(float) * size_t(d) * b, st));
+    return POETX_OK;
+  }
+  POETX_TRY(check_ptr(codes));
+  POETX_TRY(check_ptr(exps));
+  POETX_TRY(check_ptr(D));
+  if (O) POETX_TRY(check_ptr(G));
+  POETX_TRY(check_opt(O));
+  if (!ws || ws_bytes < block_backward_ws(T, d, b, dtype)) return POETX_E_WORKSPACE;
+  int dev;
+  POETX_TRY(current_device(&dev));
+  const int et = elem_type(dtype), nb = d / b;
+  const bool tc_path = use_tc(dtype);
+  const int splits = dg_splits(nb, b, T, dtype);
+  const size_t elems = size_t(d) * b;
+  Carver c(ws, ws_bytes);
+  void* X = c.take<uint8_t>(size_t(dtype_size(dtype)) * T * d);
+  float* part = c.take<float>(sizeof(float) * splits * elems);
+  POETX_CUDA(checkpoint_load(T, d, codes, exps, dtype, X, st, dev));
+  if (splits == 1 && !accumulate) part = dG;
+  if (dtype == POETX_BF16 && b == bdg2::BLK) {
+    PROFILED(ST_BDG, st, POETX_CUDA(launch_bdg(D, X, O ? G : D, O, part, T, d, splits, st, dev)));
+  } else {
+    if (O) PROFILED(ST_BLOCKDIAG, st, POETX_CUDA(launch_gemm(blockdiag_desc(D, et, T, d, b, G, true, O, et), tc_path, st, dev)));
+    PROFILED(ST_DG, st, POETX_CUDA(launch_gemm(blockgrad_desc(X, D, et, T, d, b, splits, part), tc_path, st, dev)));
+  }
+  if (part != dG) {
+    PROFILED(ST_REDUCE, st,
+             q8::add_splits_kernel<<<grid_for(static_cast<int64_t>(elems + 3) / 4, 256, dev), 256, 0, st>>>(
+                 part, splits, static_cast<int64_t>(elems), dG, accumulate));
+    POETX_CUDA(cudaGetLastError());
+  }
+  return POETX_OK;
+}
+
+}  // extern "C"
