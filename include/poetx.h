@@ -315,9 +315,13 @@ poetx_status poetx_rmsnorm_backward(int64_t T, int32_t d, const void* dy, const 
  *   out[t][j] = xscale[t] wscale[j] sum_i xq[t][i] Wq[j][i]
  * xq [T][m], Wq [n][m] int8 (any codes), xscale [T], wscale [n] fp32, out
  * [T][n] (dtype).  The sum is exact (32-bit integers); the scales are applied
- * in fp32, xscale first. */
+ * in fp32, xscale first.  No workspace is needed when m is a multiple of 16
+ * (the size is 0 then and ws may be NULL); for other m both operands are
+ * copied to padded rows there on every call. */
+size_t poetx_matmul_int8_workspace_bytes(int64_t T, int32_t n, int32_t m);
 poetx_status poetx_matmul_int8(int64_t T, int32_t n, int32_t m, const int8_t* xq, const float* xscale,
-                               const int8_t* Wq, const float* wscale, int32_t dtype, void* out, void* stream);
+                               const int8_t* Wq, const float* wscale, int32_t dtype, void* out, void* ws,
+                               size_t ws_bytes, void* stream);
 
 /* Gradient of that product with respect to its tokens, in 8 bits too: the
  * rows of dz * wscale ([T][n], each product rounded to fp32) are quantised as

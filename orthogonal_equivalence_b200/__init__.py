@@ -80,7 +80,8 @@ SIGNATURES = {
     "poetx_rmsnorm_backward_workspace_bytes": (_SZ, [_I64, _I32]),
     "poetx_rmsnorm_backward": (ctypes.c_int, [_I64, _I32, _VP, _VP, _VP, _VP, _VP, _I32, _VP, _VP, _I32, _VP, _SZ,
                                               _VP]),
-    "poetx_matmul_int8": (ctypes.c_int, [_I64, _I32, _I32, _VP, _VP, _VP, _VP, _I32, _VP, _VP]),
+    "poetx_matmul_int8_workspace_bytes": (_SZ, [_I64, _I32, _I32]),
+    "poetx_matmul_int8": (ctypes.c_int, [_I64, _I32, _I32, _VP, _VP, _VP, _VP, _I32, _VP, _VP, _SZ, _VP]),
     "poetx_matmul_int8_grad_workspace_bytes": (_SZ, [_I64, _I32, _I32]),
     "poetx_matmul_int8_grad": (ctypes.c_int, [_I64, _I32, _I32, _VP, _VP, _VP, _I32, _VP, _VP, _SZ, _VP]),
     "poetx_checkpoint_save": (ctypes.c_int, [_I64, _I32, _VP, _I32, _VP, _VP, _VP]),
@@ -292,9 +293,14 @@ def poetx_rmsnorm_backward(T: int, d: int, dy, h, gamma, rstd, dres, dtype: int,
            "poetx_rmsnorm_backward")
 
 
-def poetx_matmul_int8(T: int, n: int, m: int, xq, xscale, Wq, wscale, dtype: int, out, stream=None) -> None:
+def poetx_matmul_int8_workspace_bytes(T: int, n: int, m: int) -> int:
+    return lib().poetx_matmul_int8_workspace_bytes(T, n, m)
+
+
+def poetx_matmul_int8(T: int, n: int, m: int, xq, xscale, Wq, wscale, dtype: int, out, ws, ws_bytes: int,
+                      stream=None) -> None:
     _check(lib().poetx_matmul_int8(T, n, m, _ptr(xq), _ptr(xscale), _ptr(Wq), _ptr(wscale), dtype, _ptr(out),
-                                   _stream(stream)), "poetx_matmul_int8")
+                                   _ptr(ws), ws_bytes, _stream(stream)), "poetx_matmul_int8")
 
 
 def poetx_matmul_int8_grad_workspace_bytes(T: int, n: int, m: int) -> int:

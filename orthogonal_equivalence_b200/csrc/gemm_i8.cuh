@@ -1,82 +1,473 @@
-// Int8 products of the POET-XQ weight (codes Wq [n][m], a scale per row):
+// Int8 products of the POET-XQ weight (codes Wq [n][m], a scale per row) on
+// the tensor cores (tcgen05 kind::i8, 32-bit integer accumulators in TMEM):
 //   forward   z[t][j]  = xs[t] ws[j] sum_i xq[t][i] Wq[j][i]
 //   gradient  dx[t][i] = gs[t]       sum_j gq[t][j] Wq[j][i]
-// with the sums exact in 32-bit integers (|code| <= 128 and at most 102400
-// terms stay below 2^31).
+// The sums are exact (|code| <= 128 and at most 102400 terms stay below
+// 2^31), so neither a split of K nor its order changes a result.
+//
+// Wq is stored once, [n][m]: the forward reads it K-major, the gradient
+// MN-major (the contraction runs over its rows), both by TMA in 128-byte
+// swizzled boxes of 128 rows.
+//
+//   pair kernel: 256 x 256 tiles on CTA pairs, persistent; for many tokens.
+//   wide kernel: the weight's 128 rows are the M side of the tile and up to
+//     256 tokens its N side, K split over a cluster whose CTAs add their
+//     integer sums over distributed shared memory; for few tokens, where all
+//     SMs are needed to stream the weight.
 #pragma once
 
 #include <cstdint>
 #include <cuda_bf16.h>
 
+#include "gemm2sm.cuh"
 #include "perm.cuh"
 
 namespace poetx {
 namespace i8 {
 
-struct Params {
-  const int8_t* a;      // [M][lda] codes of the tokens
-  const int8_t* b;      // forward: [N][ldb], gradient: [K][ldb]
-  const float* as;      // [M]
-  const float* bs;      // [N] or NULL
+constexpr int KB = 128;          // K per stage: 128 codes = one 128-byte row
+constexpr int UMMA_K = 32;
+constexpr int BOX_BYTES = 128 * 128;
+
+__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_one(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 32 integers of a TMEM row: the accumulators as loaded by tmem_ld_32cols.
+__device__ __forceinline__ int as_int(float v) { return __float_as_int(v); }
+
+// ---------------------------------------------------------------- many tokens
+constexpr int STAGES = 6;
+constexpr int STAGE_BYTES = 2 * BOX_BYTES;  // this CTA's 128 tokens and 128 columns
+constexpr int EPI_BOX = 32 * 128;
+constexpr int EPI_BYTES = 4 * 2 * EPI_BOX;
+constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_BYTES + 1024 + 256;
+constexpr int NUM_THREADS = 192;
+
+struct PairParams {
+  tc2::Params g;        // sizes, raster, instruction descriptor
+  const float* as;      // [M] token scales
+  const float* bs;      // [N] channel scales or NULL
   void* out;            // [M][N]
-  int64_t lda, ldb;
-  int M, N, K;
+  int tma_out;          // rows of out are whole 16-byte units: TMA store
 };
 
-// 64 x 64 output tile, 32 bytes of K per step, 4 x 4 sums per thread by dp4a.
-constexpr int TILE = 64, KB = 32;
+// Warp roles, barriers and raster as in the bf16 W0 product (gemm2sm.cuh); a
+// stage holds twice the K in the same bytes.  The epilogue turns 32 x 128
+// bytes of output at a time (64 bf16 or 32 fp32 columns) into a swizzled box
+// and stores it by TMA, or row by row when out's rows are not 16-byte units.
+template <typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
+    product_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                        const __grid_constant__ CUtensorMap tmC, const PairParams pp) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES + EPI_BYTES);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5);
+  const tc2::Params& p = pp.g;
 
-template <typename T, bool B_KN>
-__global__ void __launch_bounds__(256) product_kernel(const Params p) {
-  __shared__ int as[TILE][KB / 4 + 1], bs[TILE][KB / 4 + 1];
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * TILE;
-  const int n0 = blockIdx.y * TILE;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  int acc[4][4] = {};
-  int8_t* a8 = reinterpret_cast<int8_t*>(as);
-  int8_t* b8 = reinterpret_cast<int8_t*>(bs);
-  constexpr int ROW = (KB / 4 + 1) * 4;
-  for (int k0 = 0; k0 < p.K; k0 += KB) {
-    for (int i = threadIdx.x; i < TILE * KB; i += 256) {
-      const int r = i / KB, k = i % KB;
-      a8[r * ROW + k] = m0 + r < p.M && k0 + k < p.K ? p.a[(m0 + r) * p.lda + k0 + k] : int8_t(0);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = tc2::cluster_rank();
+  const bool leader = rank == 0;
+  const uint32_t smem_base = smem_u32(smem);
+  const uint32_t sEpi = smem_base + STAGES * STAGE_BYTES;
+  auto bar = [&](int i) { return smem_u32(bars + i); };
+  const int FULL = 0, EMPTY = STAGES, TFULL = 2 * STAGES, TEMPTY = 2 * STAGES + 2, DRAIN = 2 * STAGES + 4;
+  constexpr int BM = tc2::BM, BN = tc2::BN;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(bar(FULL + s), 1);
+      mbar_init(bar(EMPTY + s), 1);
     }
-    for (int i = threadIdx.x; i < TILE * KB; i += 256) {
-      const int r = B_KN ? i % TILE : i / KB, k = B_KN ? i / TILE : i % KB;
-      int8_t v = 0;
-      if (n0 + r < p.N && k0 + k < p.K)
-        v = B_KN ? p.b[static_cast<int64_t>(k0 + k) * p.ldb + n0 + r] : p.b[static_cast<int64_t>(n0 + r) * p.ldb + k0 + k];
-      b8[r * ROW + k] = v;
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(bar(TFULL + a), 1);
+      mbar_init(bar(TEMPTY + a), 8);  // 4 epilogue warps x 2 CTAs
     }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < KB / 4; ++k) {
-      int av[4], bv[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        av[i] = as[ty + 16 * i][k];
-        bv[i] = bs[tx + 16 * i][k];
+    mbar_init(bar(DRAIN), 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
+                 "r"(tc2::TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  tc2::cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+
+  const int total = p.tiles_m * p.tiles_n;
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int nkb = (p.K + KB - 1) / KB;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------- TMA producer (both CTAs)
+      prefetch_tmap(&tmA);
+      prefetch_tmap(&tmB);
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int tile = pair; tile < total && ok; tile += npairs) {
+        int mt, nt;
+        tc2::decode(p, tile, mt, nt);
+        const int m0 = mt * BM + rank * 128, n0 = nt * BN + rank * 128;
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!mbar_wait(bar(EMPTY + stage), phase ^ 1u, DERR_GEMM_WAIT)) { ok = false; break; }
+          const uint32_t full_leader = tc2::map_to_rank(bar(FULL + stage), 0);
+          if (leader) mbar_arrive_expect_tx(bar(FULL + stage), 2 * STAGE_BYTES);
+          const uint32_t sa = smem_base + stage * STAGE_BYTES, sb = sa + BOX_BYTES;
+          const int k = kb * KB;
+          tc2::tma_load_2d_pair(sa, &tmA, full_leader, k, m0);
+          if (!p.b_mn) tc2::tma_load_2d_pair(sb, &tmB, full_leader, k, n0);
+          else tc2::tma_load_2d_pair(sb, &tmB, full_leader, n0, k);
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = __dp4a(av[i], bv[j], acc[i][j]);
+      if (!ok) {
+        const uint64_t t0 = global_ns();
+        while (global_ns() - t0 < 100000ull) {
+        }
+      }
     }
+  } else if (warp == 1) {
+    if (leader && lane == 0) {
+      // ---------------- MMA issuer (leader CTA, for both)
+      int stage = 0;
+      uint32_t phase = 0;
+      int local = 0;
+      bool ok = true;
+      for (int tile = pair; tile < total && ok; tile += npairs, ++local) {
+        const int acc = local & 1;
+        const uint32_t acc_phase = (local >> 1) & 1;
+        if (!mbar_wait(bar(TEMPTY + acc), acc_phase ^ 1u, DERR_GEMM_WAIT)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + acc * BN;
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!mbar_wait(bar(FULL + stage), phase, DERR_GEMM_WAIT)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t sa = smem_base + stage * STAGE_BYTES, sb = sa + BOX_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < KB / UMMA_K; ++kk)
+            mma_pair(d_tmem, smem_desc_sw128(sa + kk * UMMA_K, 16, 1024),
+                     smem_desc_sw128(sb + kk * p.b_kstep, 16, 1024), p.idesc, (kb | kk) != 0 ? 1u : 0u);
+          tc2::commit_pair(bar(EMPTY + stage));
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+        tc2::commit_pair(bar(TFULL + acc));
+      }
+      asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar(DRAIN))
+                   : "memory");
+      mbar_wait(bar(DRAIN), 0, DERR_GEMM_WAIT);
+    }
+  } else {
+    // ---------------- epilogue (both CTAs): this CTA's 128 rows of each tile
+    constexpr int CW = 128 / sizeof(T);  // columns of a box
+    const int quarter = warp & 3;
+    const uint32_t my_boxes = sEpi + (warp - 2) * 2 * EPI_BOX;
+    const uint32_t tempty_leader = tc2::map_to_rank(bar(TEMPTY), 0);
+    int buf = 0;
+    int local = 0;
+    for (int tile = pair; tile < total; tile += npairs, ++local) {
+      int mt, nt;
+      tc2::decode(p, tile, mt, nt);
+      const int acc = local & 1;
+      const uint32_t acc_phase = (local >> 1) & 1;
+      const int row0 = mt * BM + rank * 128 + quarter * 32;
+      const float as = row0 + lane < p.M ? pp.as[row0 + lane] : 0.f;
+      bool ok = mbar_wait(bar(TFULL + acc), acc_phase, DERR_GEMM_WAIT);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const bool rows_in = row0 < p.M;
+      const uint32_t tl = tmem_base + acc * BN + (static_cast<uint32_t>(quarter * 32) << 16);
+#pragma unroll 1
+      for (int c0 = 0; c0 < BN; c0 += CW) {
+        const int col0 = nt * BN + c0;
+        uint32_t w[32];
+#pragma unroll
+        for (int half = 0; half < CW / 32; ++half) {
+          float v[32];
+          tmem_ld_32cols(tl + c0 + 32 * half, v);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const int c = col0 + 32 * half + 4 * q;
+            float b[4] = {1.f, 1.f, 1.f, 1.f};
+            if (pp.bs) {
+              if (c + 4 <= p.N) {
+                const float4 f = __ldg(reinterpret_cast<const float4*>(pp.bs + c));
+                b[0] = f.x; b[1] = f.y; b[2] = f.z; b[3] = f.w;
+              } else {
+#pragma unroll
+                for (int e = 0; e < 3; ++e)
+                  if (c + e < p.N) b[e] = __ldg(pp.bs + c + e);
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[4 * q + e] = static_cast<float>(as_int(v[4 * q + e])) * as * b[e];
+          }
+          if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[16 * half + i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i]);
+          }
+        }
+        if (!rows_in || col0 >= p.N) continue;
+        if (lane == 0) bulk_wait_read<1>();
+        __syncwarp();
+        const uint32_t box = my_boxes + buf * EPI_BOX;
+        const uint32_t rowp = box + lane * 128;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(rowp + ((k ^ (lane & 7)) << 4)),
+                       "r"(w[4 * k]), "r"(w[4 * k + 1]), "r"(w[4 * k + 2]), "r"(w[4 * k + 3])
+                       : "memory");
+        if (pp.tma_out) {
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tmC, box, col0, row0);
+            bulk_commit();
+          }
+          buf ^= 1;
+        } else {
+          __syncwarp();
+          T* out = static_cast<T*>(pp.out);
+          const uint8_t* bx = smem + (box - smem_base);
+          constexpr int PER = 16 / sizeof(T);
+          const int rows = min(32, p.M - row0);
+          for (int r = 0; r < rows; ++r)
+#pragma unroll
+            for (int c = lane; c < CW; c += 32)
+              if (col0 + c < p.N)
+                out[static_cast<int64_t>(row0 + r) * p.N + col0 + c] =
+                    reinterpret_cast<const T*>(bx + r * 128 + (((c / PER) ^ (r & 7)) << 4))[c % PER];
+          __syncwarp();
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc2::remote_arrive(tempty_leader + 8 * acc);
+    }
+    if (lane == 0) bulk_wait_all();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc2::cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(tc2::TMEM_COLS)
+                 : "memory");
+  }
+  tc2::cluster_sync();
+}
+
+// ---------------------------------------------------------------- few tokens
+struct WideParams {
+  const float* as;      // [T] token scales
+  const float* bs;      // [N] scales of the weight's side or NULL
+  void* out;            // [T][N]
+  int T, N, K;
+  int nt;               // tokens per tile: 16, 32, 64, 128 or 256
+  int stages;
+  int w_mn;             // the weight's K is its rows (gradient)
+  uint32_t idesc;
+  int tmem_cols;
+};
+
+// Grid (S, ceil(N / 128), ceil(T / nt)), clusters of the S CTAs of one tile.
+// CTA s takes the K blocks [s nkb / S, (s + 1) nkb / S), S <= nkb.
+template <typename T>
+__global__ void __launch_bounds__(NUM_THREADS)
+    product_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                        const WideParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int stage_bytes = BOX_BYTES + p.nt * KB;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + p.stages * stage_bytes);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * p.stages + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t smem_base = smem_u32(smem);
+  auto full = [&](int i) { return smem_u32(bars + i); };
+  auto empty = [&](int i) { return smem_u32(bars + p.stages + i); };
+  const uint32_t done = smem_u32(bars + 2 * p.stages);
+  const int S = gridDim.x, rank = blockIdx.x;
+  const int n0 = blockIdx.y * 128, t0 = blockIdx.z * p.nt;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    mbar_init(done, 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_holder), p.tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+
+  const int nkb = (p.K + KB - 1) / KB;
+  const int k_first = static_cast<int>(int64_t(rank) * nkb / S), k_last = static_cast<int>(int64_t(rank + 1) * nkb / S);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      prefetch_tmap(&tmW);
+      prefetch_tmap(&tmX);
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int kb = k_first; kb < k_last; ++kb) {
+        if (!mbar_wait(empty(stage), phase ^ 1u, DERR_GEMM_WAIT)) {
+          const uint64_t s0 = global_ns();
+          while (global_ns() - s0 < 100000ull) {
+          }
+          break;
+        }
+        const uint32_t sw = smem_base + stage * stage_bytes;
+        mbar_arrive_expect_tx(full(stage), stage_bytes);
+        if (!p.w_mn) tma_load_2d(sw, &tmW, full(stage), kb * KB, n0);
+        else tma_load_2d(sw, &tmW, full(stage), n0, kb * KB);
+        tma_load_2d(sw + BOX_BYTES, &tmX, full(stage), kb * KB, t0);
+        if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      const int wstep = p.w_mn ? UMMA_K * 128 : UMMA_K;
+      for (int kb = k_first; kb < k_last; ++kb) {
+        if (!mbar_wait(full(stage), phase, DERR_GEMM_WAIT)) break;
+        tc_fence_after();
+        const uint32_t sw = smem_base + stage * stage_bytes, sx = sw + BOX_BYTES;
+#pragma unroll
+        for (int kk = 0; kk < KB / UMMA_K; ++kk)
+          mma_one(tmem_base, smem_desc_sw128(sw + kk * wstep, 16, 1024), smem_desc_sw128(sx + kk * UMMA_K, 16, 1024),
+                  p.idesc, (kb != k_first || kk != 0) ? 1u : 0u);
+        tc_commit(empty(stage));
+        if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+      }
+      tc_commit(done);
+    }
+  }
+  __syncwarp();
+  const int quarter = warp & 3, row = quarter * 32 + lane;
+  const int cols = min(p.nt, p.T - t0);
+  const uint32_t tl = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+  T* out = static_cast<T*>(p.out) + static_cast<int64_t>(t0) * p.N + n0;
+  const float* as = p.as + t0;
+  const bool row_in = n0 + row < p.N;
+  float bs = 1.f;
+  if (warp >= 2 && p.bs && row_in) bs = p.bs[n0 + row];
+  int* part = reinterpret_cast<int*>(smem);  // [cols][128], over the stages once every MMA has read them
+  if (warp >= 2) {
+    bool ok = mbar_wait(done, 0, DERR_GEMM_WAIT);
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok) {
+      tc_fence_after();
+      for (int c0 = 0; c0 < cols; c0 += 32) {
+        float v[32];
+        tmem_ld_32cols(tl + c0, v);
+        if (S == 1) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (c0 + i < cols && row_in)
+              out[static_cast<int64_t>(c0 + i) * p.N + row] =
+                  from_f32<T>(static_cast<float>(as_int(v[i])) * __ldg(as + c0 + i) * bs);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (c0 + i < cols) part[(c0 + i) * 128 + row] = as_int(v[i]);
+        }
+      }
+      tc_fence_before();
+    }
+  }
+  if (S > 1) {
+    // add the S integer sums of the tile: this CTA the token columns rank, rank + S, ...
+    tc2::cluster_sync();
+    if (warp >= 2 && row_in) {
+      const uint32_t mine = smem_u32(part) + row * 4;
+      for (int c = rank; c < cols; c += S) {
+        int sum = 0;
+        for (int s = 0; s < S; ++s) {
+          int v;
+          asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(tc2::map_to_rank(mine + c * 512, s)) : "memory");
+          sum += v;
+        }
+        out[static_cast<int64_t>(c) * p.N + row] = from_f32<T>(static_cast<float>(sum) * __ldg(as + c) * bs);
+      }
+    }
+    tc2::cluster_sync();  // no CTA leaves while its sums are read
+  } else {
     __syncthreads();
   }
-  T* out = static_cast<T*>(p.out);
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, p.tmem_cols);
+  }
+}
+
+// Rows of `cols` bytes copied to rows `ld` apart (ld a multiple of 16, the
+// bytes behind cols unwritten), for operands whose rows are not whole 16-byte
+// units and so cannot be read by TMA.  A thread builds 16 bytes from the five
+// aligned words that hold them.
+__global__ void __launch_bounds__(256) pad_rows_kernel(const int8_t* __restrict__ src, int64_t rows, int cols,
+                                                       int8_t* __restrict__ dst, int64_t ld) {
+  const int per = (cols + 15) / 16;
+  const int64_t n = rows * per, size = rows * cols;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int64_t r = i / per;
+    const int c = static_cast<int>(i - r * per) * 16;
+    const int64_t at = r * cols + c;
+    uint4 w;
+    uint32_t* o = reinterpret_cast<uint32_t*>(&w);
+    if (at + 20 <= size) {
+      const uint32_t* a = reinterpret_cast<const uint32_t*>(src + (at & ~int64_t(3)));
+      const uint32_t sh = static_cast<uint32_t>(at & 3) * 8;
+      uint32_t lo = a[0];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t r = m0 + ty + 16 * i;
-    if (r >= p.M) continue;
-    const float s = p.as[r];
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t hi = a[k + 1];
+        o[k] = __funnelshift_r(lo, hi, sh);
+        lo = hi;
+      }
+    } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = n0 + tx + 16 * j;
-      if (c >= p.N) continue;
-      const float v = static_cast<float>(acc[i][j]) * s;
-      out[r * p.N + c] = from_f32<T>(p.bs ? v * p.bs[c] : v);
+      for (int k = 0; k < 4; ++k) {
+        o[k] = 0;
+        for (int e = 0; e < 4; ++e)
+          if (at + 4 * k + e < size) o[k] |= static_cast<uint32_t>(static_cast<uint8_t>(src[at + 4 * k + e])) << (8 * e);
+      }
     }
+    *reinterpret_cast<uint4*>(dst + r * ld + c) = w;
   }
 }
 

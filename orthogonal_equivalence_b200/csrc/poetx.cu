@@ -1917,20 +1917,172 @@ cudaError_t checkpoint_load(int64_t T, int32_t d, const int8_t* codes, const uin
   return cudaSuccess;
 }
 
-cudaError_t product_i8(const i8::Params& p, bool b_kn, int32_t dtype, cudaStream_t st) {
-  const dim3 grid((p.M + i8::TILE - 1) / i8::TILE, (p.N + i8::TILE - 1) / i8::TILE);
-  Prof prof(ST_INT8, st);
-  if (dtype == POETX_BF16) {
-    if (b_kn) i8::product_kernel<__nv_bfloat16, true><<<grid, 256, 0, st>>>(p);
-    else i8::product_kernel<__nv_bfloat16, false><<<grid, 256, 0, st>>>(p);
-  } else {
-    if (b_kn) i8::product_kernel<float, true><<<grid, 256, 0, st>>>(p);
-    else i8::product_kernel<float, false><<<grid, 256, 0, st>>>(p);
+// ---- int8 products (gemm_i8.cuh)
+bool encode_bytes_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
+  cuuint32_t box[2] = {128u, static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// One product: out[t][j] = as[t] bs[j] sum_k a[t][k] w(j, k), with w(j, k) at
+// w[j * ldw + k], or (w_mn) at w[k * ldw + j].  lda, ldw: multiples of 16.
+struct ProductI8 {
+  const int8_t* a;
+  const int8_t* w;
+  const float* as;
+  const float* bs;
+  void* out;
+  int64_t lda, ldw;
+  int T, N, K;
+  bool w_mn;
+};
+
+struct WideShape {
+  int nt, S, stages;
+};
+
+// idesc: D int32, A and B signed 8-bit
+constexpr uint32_t kIdescI8 = (2u << 4) | (1u << 7) | (1u << 10);
+
+template <typename T>
+cudaError_t launch_wide_i8(const ProductI8& q, const WideShape& w, cudaStream_t st, int device) {
+  static bool attr_set[64] = {false};
+  if (device >= 0 && device < 64 && !attr_set[device]) {
+    const cudaError_t e = cudaFuncSetAttribute(i8::product_wide_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               227 * 1024);
+    if (e != cudaSuccess) return e;
+    attr_set[device] = true;
   }
+  CUtensorMap mw, mx;
+  const int64_t wrows = q.w_mn ? q.K : q.N, wcols = q.w_mn ? q.N : q.K;
+  if (!encode_bytes_map(&mw, q.w, wrows, wcols, q.ldw, 128) || !encode_bytes_map(&mx, q.a, q.T, q.K, q.lda, w.nt))
+    return cudaErrorInvalidValue;
+  i8::WideParams p;
+  p.as = q.as;
+  p.bs = q.bs;
+  p.out = q.out;
+  p.T = q.T;
+  p.N = q.N;
+  p.K = q.K;
+  p.nt = w.nt;
+  p.stages = w.stages;
+  p.w_mn = q.w_mn ? 1 : 0;
+  p.idesc = kIdescI8 | (static_cast<uint32_t>(p.w_mn) << 15) | (static_cast<uint32_t>(w.nt >> 3) << 17) | (8u << 24);
+  p.tmem_cols = w.nt < 32 ? 32 : w.nt;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(w.S, (q.N + 127) / 128, (q.T + w.nt - 1) / w.nt);
+  cfg.blockDim = dim3(i8::NUM_THREADS);
+  cfg.dynamicSmemBytes = size_t(w.stages) * (i8::BOX_BYTES + w.nt * i8::KB) + 1024 + 256;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = w.S;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, i8::product_wide_kernel<T>, mw, mx, p);
+}
+
+template <typename T>
+cudaError_t launch_pair_i8(const ProductI8& q, cudaStream_t st, int device) {
+  static bool attr_set[64] = {false};
+  if (device >= 0 && device < 64 && !attr_set[device]) {
+    const cudaError_t e = cudaFuncSetAttribute(i8::product_pair_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               i8::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    attr_set[device] = true;
+  }
+  CUtensorMap ma, mb, mc;
+  const int64_t wrows = q.w_mn ? q.K : q.N, wcols = q.w_mn ? q.N : q.K;
+  if (!encode_bytes_map(&ma, q.a, q.T, q.K, q.lda, 128) || !encode_bytes_map(&mb, q.w, wrows, wcols, q.ldw, 128))
+    return cudaErrorInvalidValue;
+  i8::PairParams pp;
+  pp.tma_out = (int64_t(q.N) * sizeof(T)) % 16 == 0;
+  if (pp.tma_out) {
+    Operand2D cv;
+    cv.ptr = q.out;
+    cv.et = sizeof(T) == 2 ? ET_BF16 : ET_F32;
+    cv.rows = q.T;
+    cv.cols = q.N;
+    cv.ld = q.N;
+    if (!encode_map(&mc, cv, 32)) return cudaErrorInvalidValue;
+  } else {
+    mc = ma;  // unused
+  }
+  tc2::Params& p = pp.g;
+  p.M = q.T;
+  p.N = q.N;
+  p.K = q.K;
+  p.tiles_m = (q.T + tc2::BM - 1) / tc2::BM;
+  p.tiles_n = (q.N + tc2::BN - 1) / tc2::BN;
+  p.b_mn = q.w_mn ? 1 : 0;
+  p.idesc = kIdescI8 | (static_cast<uint32_t>(p.b_mn) << 16) | (static_cast<uint32_t>(tc2::BN >> 3) << 17) |
+            (static_cast<uint32_t>(tc2::BM >> 4) << 24);
+  p.b_kstep = q.w_mn ? i8::UMMA_K * 128 : i8::UMMA_K;
+  p.b_lbo = 16;
+  p.alpha = 1.f;
+  choose_raster(p);
+  pp.as = q.as;
+  pp.bs = q.bs;
+  pp.out = q.out;
+  const int tiles = p.tiles_m * p.tiles_n;
+  const int pairs = sm_count(device) / 2;
+  i8::product_pair_kernel<T><<<2 * (tiles < pairs ? tiles : pairs), i8::NUM_THREADS, i8::SMEM_BYTES, st>>>(ma, mb, mc,
+                                                                                                         pp);
   return cudaGetLastError();
 }
 
-size_t grad_i8_ws(int64_t T, int32_t n) { return kAlign + al(size_t(T) * n) + al(sizeof(float) * size_t(T)); }
+WideShape wide_shape(int T, int N, int K, int device) {
+  WideShape w;
+  w.nt = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : 256;
+  const int per_sm = w.nt <= 32 ? 4 : w.nt <= 128 ? 2 : 1;   // CTAs an SM holds
+  w.stages = w.nt <= 32 ? (w.nt == 16 ? 3 : 2) : w.nt == 64 ? 4 : w.nt == 128 ? 3 : 4;
+  const int64_t tiles = int64_t((N + 127) / 128) * ((T + w.nt - 1) / w.nt);
+  const int nkb = (K + i8::KB - 1) / i8::KB;
+  int64_t S = int64_t(sm_count(device)) * per_sm / tiles;
+  if (S > nkb / 2) S = nkb / 2;
+  if (S > 8) S = 8;
+  w.S = S < 1 ? 1 : static_cast<int>(S);
+  return w;
+}
+
+cudaError_t product_i8(const ProductI8& q, int32_t dtype, cudaStream_t st, int device) {
+  const int64_t tiles = int64_t((q.T + 255) / 256) * ((q.N + 255) / 256);
+  bool pair = q.T > 256 && 2 * tiles >= sm_count(device);
+  WideShape w = wide_shape(q.T, q.N, q.K, device);
+#ifdef TUNE
+  if (const char* e = getenv("I8P")) pair = atoi(e);
+  if (const char* e = getenv("I8W")) sscanf(e, "%d,%d,%d", &w.nt, &w.S, &w.stages);
+#endif
+  Prof prof(ST_INT8, st);
+  if (pair)
+    return dtype == POETX_BF16 ? launch_pair_i8<__nv_bfloat16>(q, st, device) : launch_pair_i8<float>(q, st, device);
+  return dtype == POETX_BF16 ? launch_wide_i8<__nv_bfloat16>(q, w, st, device) : launch_wide_i8<float>(q, w, st, device);
+}
+
+int64_t row16(int64_t cols) { return (cols + 15) / 16 * 16; }
+
+cudaError_t pad_rows(const int8_t* src, int64_t rows, int cols, int8_t* dst, cudaStream_t st, int device) {
+  const int64_t n = rows * ((cols + 15) / 16);
+  PROFILED(ST_INT8, st,
+           i8::pad_rows_kernel<<<grid_for(n, 256, device), 256, 0, st>>>(src, rows, cols, dst, row16(cols)));
+  return cudaGetLastError();
+}
+
+// Copies of operands whose rows are not whole 16-byte units (TMA's rule).
+size_t product_i8_ws(int64_t T, int32_t n, int32_t m) {
+  return m % 16 ? kAlign + al(size_t(T) * row16(m)) + al(size_t(n) * row16(m)) : 0;
+}
+size_t grad_i8_ws(int64_t T, int32_t n, int32_t m) {
+  return kAlign + al(size_t(T) * row16(n)) + al(sizeof(float) * size_t(T)) + (m % 16 ? al(size_t(n) * row16(m)) : 0);
+}
 
 size_t block_backward_ws(int64_t T, int32_t d, int32_t b, int32_t dtype) {
   return kAlign + al(size_t(dtype_size(dtype)) * T * d) +
@@ -2038,24 +2190,43 @@ poetx_status poetx_rmsnorm_backward(int64_t T, int32_t d, const void* dy, const 
   return POETX_OK;
 }
 
+size_t poetx_matmul_int8_workspace_bytes(int64_t T, int32_t n, int32_t m) {
+  if (check_rows(T, n, kMaxD8) != POETX_OK || check_rows(T, m, kMaxD8) != POETX_OK) return 0;
+  return product_i8_ws(T, n, m);
+}
+
 poetx_status poetx_matmul_int8(int64_t T, int32_t n, int32_t m, const int8_t* xq, const float* xscale,
-                               const int8_t* Wq, const float* wscale, int32_t dtype, void* out, void* stream) {
+                               const int8_t* Wq, const float* wscale, int32_t dtype, void* out, void* ws,
+                               size_t ws_bytes, void* stream) {
   POETX_TRY(check_dtype(dtype));
   POETX_TRY(check_rows(T, m, kMaxD8));
   POETX_TRY(check_rows(T, n, kMaxD8));
   if (T == 0) return POETX_OK;
   const void* need[] = {xq, xscale, Wq, wscale, out};
   for (const void* p : need) POETX_TRY(check_ptr(p));
+  const size_t ws_need = product_i8_ws(T, n, m);
+  if (ws_need && (!ws || ws_bytes < ws_need)) return POETX_E_WORKSPACE;
   int dev;
   POETX_TRY(current_device(&dev));
-  i8::Params p{xq, Wq, xscale, wscale, out, m, m, static_cast<int>(T), n, m};
-  POETX_CUDA(product_i8(p, false, dtype, static_cast<cudaStream_t>(stream)));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  ProductI8 q{xq, Wq, xscale, wscale, out, m, m, static_cast<int>(T), n, m, false};
+  if (m % 16) {
+    Carver c(ws, ws_bytes);
+    int8_t* x16 = c.take<int8_t>(size_t(T) * row16(m));
+    int8_t* w16 = c.take<int8_t>(size_t(n) * row16(m));
+    POETX_CUDA(pad_rows(xq, T, m, x16, st, dev));
+    POETX_CUDA(pad_rows(Wq, n, m, w16, st, dev));
+    q.a = x16;
+    q.w = w16;
+    q.lda = q.ldw = row16(m);
+  }
+  POETX_CUDA(product_i8(q, dtype, st, dev));
   return POETX_OK;
 }
 
 size_t poetx_matmul_int8_grad_workspace_bytes(int64_t T, int32_t n, int32_t m) {
   if (check_rows(T, n, kMaxD8) != POETX_OK || check_rows(T, m, kMaxD8) != POETX_OK) return 0;
-  return grad_i8_ws(T, n);
+  return grad_i8_ws(T, n, m);
 }
 
 poetx_status poetx_matmul_int8_grad(int64_t T, int32_t n, int32_t m, const void* dz, const int8_t* Wq,
@@ -2067,16 +2238,22 @@ poetx_status poetx_matmul_int8_grad(int64_t T, int32_t n, int32_t m, const void*
   if (T == 0) return POETX_OK;
   const void* need[] = {dz, Wq, wscale, dx};
   for (const void* p : need) POETX_TRY(check_ptr(p));
-  if (!ws || ws_bytes < grad_i8_ws(T, n)) return POETX_E_WORKSPACE;
+  if (!ws || ws_bytes < grad_i8_ws(T, n, m)) return POETX_E_WORKSPACE;
   int dev;
   POETX_TRY(current_device(&dev));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   Carver c(ws, ws_bytes);
-  int8_t* gq = c.take<int8_t>(size_t(T) * n);
+  int8_t* gq = c.take<int8_t>(size_t(T) * row16(n));
   float* gs = c.take<float>(sizeof(float) * size_t(T));
-  POETX_CUDA(quantize_rows(T, n, dz, dtype, wscale, gq, n, gs, st, dev));
-  i8::Params p{gq, Wq, gs, nullptr, dx, n, m, static_cast<int>(T), m, n};
-  POETX_CUDA(product_i8(p, true, dtype, st));
+  POETX_CUDA(quantize_rows(T, n, dz, dtype, wscale, gq, row16(n), gs, st, dev));
+  ProductI8 q{gq, Wq, gs, nullptr, dx, row16(n), m, static_cast<int>(T), m, n, true};
+  if (m % 16) {
+    int8_t* w16 = c.take<int8_t>(size_t(n) * row16(m));
+    POETX_CUDA(pad_rows(Wq, n, m, w16, st, dev));
+    q.w = w16;
+    q.ldw = row16(m);
+  }
+  POETX_CUDA(product_i8(q, dtype, st, dev));
   return POETX_OK;
 }
 

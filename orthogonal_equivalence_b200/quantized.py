@@ -18,7 +18,8 @@ from typing import NamedTuple, Optional, Tuple
 import torch
 
 from . import (POETX_BF16, POETX_FP32, _check, lib, poetx_block_backward_workspace_bytes,
-               poetx_matmul_int8_grad_workspace_bytes, poetx_rmsnorm_backward_workspace_bytes)
+               poetx_matmul_int8_grad_workspace_bytes, poetx_matmul_int8_workspace_bytes,
+               poetx_rmsnorm_backward_workspace_bytes)
 
 _DTYPE = {torch.bfloat16: POETX_BF16, torch.float32: POETX_FP32}
 
@@ -175,8 +176,10 @@ def matmul_int8(xq: torch.Tensor, xscale: torch.Tensor, Wq: torch.Tensor, wscale
     if dtype not in _DTYPE:
         raise ValueError(f"dtype: {dtype}, expected torch.bfloat16 or torch.float32")
     out = torch.empty((T, n), dtype=dtype, device=dev)
+    nb = poetx_matmul_int8_workspace_bytes(T, n, m)
+    ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
     _run(dev, "poetx_matmul_int8", T, n, m, xq.data_ptr(), xscale.data_ptr(), Wq.data_ptr(), wscale.data_ptr(),
-         _DTYPE[dtype], out.data_ptr())
+         _DTYPE[dtype], out.data_ptr(), _p(ws), nb)
     return out
 
 

@@ -52,12 +52,16 @@ def test_statuses_of_the_norm(lib):
 
 def test_statuses_of_the_products(lib):
     f = lib.poetx_matmul_int8
-    assert f(4, 64, 64, P, P, P, P, 3, P, None) == 3
-    assert f(4, 102401, 64, P, P, P, P, 1, P, None) == 2
-    assert f(4, 64, 102401, P, P, P, P, 1, P, None) == 2
-    assert f(4, 64, 0, P, P, P, P, 1, P, None) == 1
-    assert f(4, 64, 64, P, None, P, P, 1, P, None) == 1
-    assert f(4, 64, 64, P, P, ODD, P, 1, P, None) == 4
+    assert f(4, 64, 64, P, P, P, P, 3, P, None, 0, None) == 3
+    assert f(4, 102401, 64, P, P, P, P, 1, P, None, 0, None) == 2
+    assert f(4, 64, 102401, P, P, P, P, 1, P, None, 0, None) == 2
+    assert f(4, 64, 0, P, P, P, P, 1, P, None, 0, None) == 1
+    assert f(4, 64, 64, P, None, P, P, 1, P, None, 0, None) == 1
+    assert f(4, 64, 64, P, P, ODD, P, 1, P, None, 0, None) == 4
+    need = px.poetx_matmul_int8_workspace_bytes(4, 64, 65)
+    assert need > 0 and px.poetx_matmul_int8_workspace_bytes(4, 64, 64) == 0
+    assert f(4, 64, 65, P, P, P, P, 1, P, P, need - 1, None) == 5
+    assert f(4, 64, 65, P, P, P, P, 1, P, None, need, None) == 5
     g = lib.poetx_matmul_int8_grad
     need = px.poetx_matmul_int8_grad_workspace_bytes(4, 64, 64)
     assert need > 0 and px.poetx_matmul_int8_grad_workspace_bytes(4, 0, 64) == 0

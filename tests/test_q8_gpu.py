@@ -261,7 +261,7 @@ def test_matmul_int8_leaves_what_lies_behind():
     xq, Wq, xs, ws = codes(27, T, m), codes(28, n, m), rnd(29, T).abs(), rnd(30, n).abs()
     for dtype, pd in ((BF, px.POETX_BF16), (F32, px.POETX_FP32)):
         big = torch.full((T + 3, n), 7.0, dtype=dtype, device="cuda")
-        px.poetx_matmul_int8(T, n, m, xq, xs, Wq, ws, pd, big)
+        px.poetx_matmul_int8(T, n, m, xq, xs, Wq, ws, pd, big, None, 0)
         assert torch.equal(big[:T], px.matmul_int8(xq, xs, Wq, ws, dtype)) and (big[T:] == 7).all()
 
 
