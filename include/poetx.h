@@ -304,9 +304,9 @@ poetx_status poetx_rmsnorm_quantize(int64_t T, int32_t d, const void* x, const v
  * that reaches h past the norm), with p = dy * gamma:
  *   dx = rstd (p - h rstd^2 mean(p h)) + dres   (dtype; of x and of residual)
  *   dgamma [d] (fp32) = sum over tokens of dy h rstd, overwritten, or added to
- *   when accumulate != 0; the sum's order depends on (T, d) alone.
+ *   when accumulate != 0; the sum's order depends on (T, d, dtype) alone.
  * T = 0 clears dgamma unless accumulate is set.  dx may be dy, h or dres. */
-size_t poetx_rmsnorm_backward_workspace_bytes(int64_t T, int32_t d);
+size_t poetx_rmsnorm_backward_workspace_bytes(int64_t T, int32_t d, int32_t dtype);
 poetx_status poetx_rmsnorm_backward(int64_t T, int32_t d, const void* dy, const void* h, const float* gamma,
                                     const float* rstd, const void* dres, int32_t dtype, void* dx, float* dgamma,
                                     int32_t accumulate, void* ws, size_t ws_bytes, void* stream);

@@ -77,7 +77,7 @@ SIGNATURES = {
     "poetx_quantize_rows": (ctypes.c_int, [_I64, _I32, _VP, _I32, _VP, _VP, _VP, _VP]),
     "poetx_rmsnorm_quantize": (ctypes.c_int, [_I64, _I32, _VP, _VP, _VP, ctypes.c_float, _I32, _VP, _VP, _VP, _VP,
                                               _VP, _VP]),
-    "poetx_rmsnorm_backward_workspace_bytes": (_SZ, [_I64, _I32]),
+    "poetx_rmsnorm_backward_workspace_bytes": (_SZ, [_I64, _I32, _I32]),
     "poetx_rmsnorm_backward": (ctypes.c_int, [_I64, _I32, _VP, _VP, _VP, _VP, _VP, _I32, _VP, _VP, _I32, _VP, _SZ,
                                               _VP]),
     "poetx_matmul_int8_workspace_bytes": (_SZ, [_I64, _I32, _I32]),
@@ -282,8 +282,8 @@ def poetx_rmsnorm_quantize(T: int, d: int, x, residual, gamma, eps: float, dtype
            "poetx_rmsnorm_quantize")
 
 
-def poetx_rmsnorm_backward_workspace_bytes(T: int, d: int) -> int:
-    return lib().poetx_rmsnorm_backward_workspace_bytes(T, d)
+def poetx_rmsnorm_backward_workspace_bytes(T: int, d: int, dtype: int) -> int:
+    return lib().poetx_rmsnorm_backward_workspace_bytes(T, d, dtype)
 
 
 def poetx_rmsnorm_backward(T: int, d: int, dy, h, gamma, rstd, dres, dtype: int, dx, dgamma, accumulate: int, ws,

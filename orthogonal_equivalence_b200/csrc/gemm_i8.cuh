@@ -11,7 +11,7 @@
 //
 //   pair kernel: 256 x 256 tiles on CTA pairs, persistent; for many tokens.
 //   wide kernel: the weight's 128 rows are the M side of the tile and up to
-//     256 tokens its N side, K split over a cluster whose CTAs add their
+//     128 tokens its N side, K split over a cluster whose CTAs add their
 //     integer sums over distributed shared memory; for few tokens, where all
 //     SMs are needed to stream the weight.
 #pragma once
@@ -290,7 +290,7 @@ struct WideParams {
   const float* bs;      // [N] scales of the weight's side or NULL
   void* out;            // [T][N]
   int T, N, K;
-  int nt;               // tokens per tile: 16, 32, 64, 128 or 256
+  int nt;               // tokens per tile: 16, 32, 64 or 128
   int stages;
   int w_mn;             // the weight's K is its rows (gradient)
   uint32_t idesc;
@@ -298,7 +298,11 @@ struct WideParams {
 };
 
 // Grid (S, ceil(N / 128), ceil(T / nt)), clusters of the S CTAs of one tile.
-// CTA s takes the K blocks [s nkb / S, (s + 1) nkb / S), S <= nkb.
+// CTA s takes the K blocks [s nkb / S, (s + 1) nkb / S), S <= nkb.  For a few
+// tokens the weight's bytes bound it: 1 x 4096 -> 14336 takes 13.2 us (9.0 at
+// the copy rate), 48 x 14336 -> 4096 16.4 us; what is left over is the launch,
+// the first loads' way and the sums' exchange.  With more tokens the epilogue
+// (one weight row a thread) counts, which is why the tiles stay narrow.
 template <typename T>
 __global__ void __launch_bounds__(NUM_THREADS)
     product_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
@@ -316,6 +320,17 @@ __global__ void __launch_bounds__(NUM_THREADS)
   const int S = gridDim.x, rank = blockIdx.x;
   const int n0 = blockIdx.y * 128, t0 = blockIdx.z * p.nt;
 
+  const int nkb = (p.K + KB - 1) / KB;
+  const int k_first = static_cast<int>(int64_t(rank) * nkb / S), k_last = static_cast<int>(int64_t(rank + 1) * nkb / S);
+
+  auto load = [&](int kb, int stage) {
+    const uint32_t sw = smem_base + stage * stage_bytes;
+    mbar_arrive_expect_tx(full(stage), stage_bytes);
+    if (!p.w_mn) tma_load_2d(sw, &tmW, full(stage), kb * KB, n0);
+    else tma_load_2d(sw, &tmW, full(stage), n0, kb * KB);
+    tma_load_2d(sw + BOX_BYTES, &tmX, full(stage), kb * KB, t0);
+  };
+  const int k_early = min(k_last, k_first + p.stages);
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(full(s), 1);
@@ -323,6 +338,9 @@ __global__ void __launch_bounds__(NUM_THREADS)
     }
     mbar_init(done, 1);
     fence_barrier_init();
+    fence_async_smem();
+    // the first round of loads flies while TMEM is allocated
+    for (int kb = k_first; kb < k_early; ++kb) load(kb, kb - k_first);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_holder), p.tmem_cols);
@@ -333,27 +351,18 @@ __global__ void __launch_bounds__(NUM_THREADS)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
 
-  const int nkb = (p.K + KB - 1) / KB;
-  const int k_first = static_cast<int>(int64_t(rank) * nkb / S), k_last = static_cast<int>(int64_t(rank + 1) * nkb / S);
-
   if (warp == 0) {
     if (lane == 0) {
-      prefetch_tmap(&tmW);
-      prefetch_tmap(&tmX);
       int stage = 0;
-      uint32_t phase = 0;
-      for (int kb = k_first; kb < k_last; ++kb) {
-        if (!mbar_wait(empty(stage), phase ^ 1u, DERR_GEMM_WAIT)) {
+      uint32_t phase = 0;  // the slot's first reader has to be done
+      for (int kb = k_early; kb < k_last; ++kb) {
+        if (!mbar_wait(empty(stage), phase, DERR_GEMM_WAIT)) {
           const uint64_t s0 = global_ns();
           while (global_ns() - s0 < 100000ull) {
           }
           break;
         }
-        const uint32_t sw = smem_base + stage * stage_bytes;
-        mbar_arrive_expect_tx(full(stage), stage_bytes);
-        if (!p.w_mn) tma_load_2d(sw, &tmW, full(stage), kb * KB, n0);
-        else tma_load_2d(sw, &tmW, full(stage), n0, kb * KB);
-        tma_load_2d(sw + BOX_BYTES, &tmX, full(stage), kb * KB, t0);
+        load(kb, stage);
         if (++stage == p.stages) { stage = 0; phase ^= 1u; }
       }
     }

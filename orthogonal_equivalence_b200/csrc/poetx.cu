@@ -1703,6 +1703,39 @@ extern "C" poetx_status poetx_selftest_wait_timeout(uint32_t limit_us, unsigned 
 }
 
 // ---------------------------------------------------------------- POET-XQ weight storage
+namespace {
+// Calls f with the columns a lane takes in the checkpoint and expansion
+// kernels (see there) and their grid.
+template <typename T, bool SAVE, typename F>
+cudaError_t with_chunks(int64_t rows, int d, int device, F f) {
+  auto grid = [&](int cols) {
+    const int gx = (d + 4 * cols - 1) / (4 * cols);
+    int64_t gy = (int64_t(sm_count(device)) * 64 + gx - 1) / gx;  // four blocks' worth for each of the 16 a SM holds
+    if (gy > rows) gy = rows;
+    return dim3(gx, static_cast<unsigned>(gy > 65535 ? 65535 : gy));
+  };
+  using std::integral_constant;
+  // fp32 rows of 4096: saving takes 53 us with 8 columns a lane and 66 with 4, expanding 81 and 64
+  if (sizeof(T) == 4 && SAVE && d % 8 == 0) return f(integral_constant<int, 8>(), grid(q8::chunk_cols<8>));
+  if (sizeof(T) == 4 && d % 4 == 0) return f(integral_constant<int, 4>(), grid(q8::chunk_cols<4>));
+  if constexpr (sizeof(T) == 2) {
+    if (d % 16 == 0) return f(integral_constant<int, 16>(), grid(q8::chunk_cols<16>));
+    if (d % 8 == 0) return f(integral_constant<int, 8>(), grid(q8::chunk_cols<8>));
+  }
+  return f(integral_constant<int, 1>(), grid(q8::chunk_cols<1>));
+}
+
+template <typename T>
+cudaError_t launch_expand(const int8_t* codes, const uint8_t* exps, const float* scale, int64_t rows, int d, void* x,
+                          cudaStream_t st, int device) {
+  return with_chunks<T, false>(rows, d, device, [&](auto N, dim3 grid) {
+    if constexpr (!(sizeof(T) == 2 && decltype(N)::value == 4))
+      q8::expand_kernel<T, decltype(N)::value><<<grid, 128, 0, st>>>(codes, exps, scale, rows, d, static_cast<T*>(x));
+    return cudaGetLastError();
+  });
+}
+}  // namespace
+
 extern "C" poetx_status poetx_weight_quantize(int32_t n, int32_t m, const void* W, int32_t dtype, int8_t* Wq,
                                               float* scale, void* stream) {
   if (dtype != POETX_FP32 && dtype != POETX_BF16) return POETX_E_DTYPE;
@@ -1734,20 +1767,9 @@ extern "C" poetx_status poetx_weight_dequantize(int32_t n, int32_t m, const int8
   int dev;
   POETX_TRY(current_device(&dev));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int64_t total = int64_t(n) * m;
-  if (dtype == POETX_BF16 && m % 16 == 0) {
-    PROFILED(ST_DEQUANT, st,
-             dequantize_rows_bf16x16_kernel<<<grid_for(total / 16, 256, dev), 256, 0, st>>>(
-                 Wq, scale, n, m, static_cast<__nv_bfloat16*>(W)));
-  } else if (dtype == POETX_BF16) {
-    PROFILED(ST_DEQUANT, st,
-             dequantize_rows_kernel<<<grid_for(total, 256, dev), 256, 0, st>>>(Wq, scale, n, m,
-                                                                              static_cast<__nv_bfloat16*>(W)));
-  } else {
-    PROFILED(ST_DEQUANT, st,
-             dequantize_rows_kernel<<<grid_for(total, 256, dev), 256, 0, st>>>(Wq, scale, n, m, static_cast<float*>(W)));
-  }
-  POETX_CUDA(cudaGetLastError());
+  PROFILED(ST_DEQUANT, st,
+           POETX_CUDA(dtype == POETX_BF16 ? launch_expand<__nv_bfloat16>(Wq, nullptr, scale, n, m, W, st, dev)
+                                          : launch_expand<float>(Wq, nullptr, scale, n, m, W, st, dev)));
   return POETX_OK;
 }
 
@@ -1789,43 +1811,88 @@ poetx_status check_rows(int64_t T, int32_t d, int32_t max_d) {
 
 poetx_status check_opt(const void* p) { return aligned16(p) ? POETX_OK : POETX_E_ALIGN; }
 
-// Threads and registers of a row: V = 8 elements a load where the row length
-// allows (16-byte rows), E elements a thread, at most 512 threads; wider rows
-// (E = 0) are read twice.
+// Threads and registers of a row: 16-byte vectors (V = 8) where the row length
+// allows, K times eight elements a thread (more where the threads of a block
+// would not do); wider rows (K = 0) are read twice.  K trades the fixed work
+// of a row (reduction, scale: ~150 instructions a warp) against registers;
+// at 16384 x 4096 bf16, K = 1, 2, 4: rows to int8 50, 51, 45 us, norm 117, 90,
+// 90 us, its backward 92 (two blocks of 512 threads), 88, 150 us.
 struct RowShape {
-  int V, E, threads;
+  int V, K, threads;
+  bool full;
 };
-RowShape row_shape(int d) {
+RowShape row_shape(int d, int k) {
   RowShape r;
   r.V = d % 8 == 0 ? 8 : 1;
-  r.E = d <= 8 * 512 ? 8 : d <= 16 * 512 ? 16 : d <= 32 * 512 ? 32 : 0;
-  const int per = r.E ? r.E : 32;
-  const int t = ((d + per - 1) / per + 31) / 32 * 32;
-  r.threads = t < 512 ? t : 512;
+  if (r.V == 1 && k > 1) k /= 2;
+  while (k < 4 && d > k * 8 * q8::kRowThreads) k *= 2;
+  r.K = d <= k * 8 * q8::kRowThreads ? k : 0;
+  const int t = ((d + 8 * k - 1) / (8 * k) + 31) / 32 * 32;
+  r.threads = t < q8::kRowThreads ? t : q8::kRowThreads;
+  r.full = r.K > 0 && r.V == 8 && d == r.threads * 8 * r.K;
+  return r;
+}
+RowShape quantize_shape(int d, int32_t dtype) { return row_shape(d, dtype == POETX_BF16 ? 4 : 2); }
+RowShape norm_shape(int d, int32_t dtype) { return row_shape(d, dtype == POETX_BF16 ? 2 : 1); }
+RowShape norm_grad_shape(int d, int32_t dtype) {
+  RowShape r = row_shape(d, dtype == POETX_BF16 ? 2 : 1);
+  if (dtype == POETX_FP32 && r.K == 4) {  // four times eight fp32 elements of three arrays do not fit the registers
+    r.K = 0;
+    r.full = false;
+  }
   return r;
 }
 
-int row_grid(int64_t T, int threads, int device) {
-  const int64_t g = int64_t(sm_count(device)) * (2048 / threads);
-  return static_cast<int>(T < g ? T : g);
+// Calls f with the template arguments (V, K, FULL) of a shape.
+template <typename F>
+cudaError_t with_shape(const RowShape& r, F f) {
+  using std::integral_constant;
+#define POETX_SHAPE(V_, K_, FULL_) \
+  if (r.V == V_ && r.K == K_ && r.full == FULL_) \
+    return f(integral_constant<int, V_>(), integral_constant<int, K_>(), integral_constant<bool, FULL_>())
+  POETX_SHAPE(8, 1, true);
+  POETX_SHAPE(8, 2, true);
+  POETX_SHAPE(8, 4, true);
+  POETX_SHAPE(8, 1, false);
+  POETX_SHAPE(8, 2, false);
+  POETX_SHAPE(8, 4, false);
+  POETX_SHAPE(8, 0, false);
+  POETX_SHAPE(1, 1, false);
+  POETX_SHAPE(1, 2, false);
+  POETX_SHAPE(1, 4, false);
+  POETX_SHAPE(1, 0, false);
+#undef POETX_SHAPE
+  return cudaErrorInvalidValue;
+}
+
+// Blocks of `threads` a SM holds of a kernel, by its registers.
+template <typename K>
+cudaError_t blocks_per_sm(K kernel, int threads, int* regs_of, int* out) {
+  if (*regs_of == 0) {
+    cudaFuncAttributes a;
+    const cudaError_t e = cudaFuncGetAttributes(&a, kernel);
+    if (e != cudaSuccess) return e;
+    *regs_of = (a.numRegs + 7) / 8 * 8;
+  }
+  const int by_regs = 65536 / (*regs_of * threads), by_threads = 2048 / threads;
+  *out = by_regs < 1 ? 1 : by_regs < by_threads ? by_regs : by_threads < 32 ? by_threads : 32;
+  return cudaSuccess;
 }
 
 template <typename T, bool NORM>
 cudaError_t launch_rows(const q8::RowsParams& p, cudaStream_t st, int device) {
-  const RowShape r = row_shape(p.d);
-  const int grid = row_grid(p.T, r.threads, device);
-  if (r.V == 8) {
-    if (r.E == 8) q8::rows_kernel<T, NORM, 8, 1><<<grid, r.threads, 0, st>>>(p);
-    else if (r.E == 16) q8::rows_kernel<T, NORM, 8, 2><<<grid, r.threads, 0, st>>>(p);
-    else if (r.E == 32) q8::rows_kernel<T, NORM, 8, 4><<<grid, r.threads, 0, st>>>(p);
-    else q8::rows_kernel<T, NORM, 8, 0><<<grid, r.threads, 0, st>>>(p);
-  } else {
-    if (r.E == 8) q8::rows_kernel<T, NORM, 1, 8><<<grid, r.threads, 0, st>>>(p);
-    else if (r.E == 16) q8::rows_kernel<T, NORM, 1, 16><<<grid, r.threads, 0, st>>>(p);
-    else if (r.E == 32) q8::rows_kernel<T, NORM, 1, 32><<<grid, r.threads, 0, st>>>(p);
-    else q8::rows_kernel<T, NORM, 1, 0><<<grid, r.threads, 0, st>>>(p);
-  }
-  return cudaGetLastError();
+  const int32_t dt = sizeof(T) == 2 ? POETX_BF16 : POETX_FP32;
+  const RowShape r = NORM ? norm_shape(p.d, dt) : quantize_shape(p.d, dt);
+  return with_shape(r, [&](auto V, auto K, auto FULL) {
+    auto kernel = q8::rows_kernel<T, NORM, decltype(V)::value, decltype(K)::value, decltype(FULL)::value>;
+    static int regs[64] = {0};
+    int per_sm;
+    const cudaError_t e = blocks_per_sm(kernel, r.threads, &regs[device & 63], &per_sm);
+    if (e != cudaSuccess) return e;
+    const int64_t g = int64_t(sm_count(device)) * per_sm;
+    kernel<<<static_cast<int>(p.T < g ? p.T : g), r.threads, 0, st>>>(p);
+    return cudaGetLastError();
+  });
 }
 
 template <bool NORM>
@@ -1851,69 +1918,48 @@ cudaError_t quantize_rows(int64_t T, int32_t d, const void* x, int32_t dtype, co
 // Blocks of the norm's backward: a fixed number, so that the sums of dgamma
 // do not depend on the device.
 int norm_grad_grid(int64_t T, int threads) {
-  const int64_t g = int64_t(kSplitSMs) * (1024 / threads < 1 ? 1 : 1024 / threads);
+  const int per_sm = 512 / threads;
+  const int64_t g = int64_t(kSplitSMs) * (per_sm < 1 ? 1 : per_sm > 16 ? 16 : per_sm);
   return static_cast<int>(T < g ? T : g);
-}
-
-template <typename T, int V, int K>
-cudaError_t launch_norm_grad_k(const q8::NormGradParams& p, int grid, int threads, cudaStream_t st, int device) {
-  const size_t smem = K > 0 ? 0 : sizeof(float) * size_t(p.d);
-  static bool attr[64] = {false};
-  cudaError_t e = allow_smem(q8::norm_grad_kernel<T, V, K>, smem, &attr[device & 63]);
-  if (e != cudaSuccess) return e;
-  q8::norm_grad_kernel<T, V, K><<<grid, threads, smem, st>>>(p);
-  return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t launch_norm_grad(const q8::NormGradParams& p, int grid, const RowShape& r, cudaStream_t st, int device) {
-  if (r.V == 8) {
-    if (r.E == 8) return launch_norm_grad_k<T, 8, 1>(p, grid, r.threads, st, device);
-    if (r.E == 16) return launch_norm_grad_k<T, 8, 2>(p, grid, r.threads, st, device);
-    if (r.E == 32) return launch_norm_grad_k<T, 8, 4>(p, grid, r.threads, st, device);
-    return launch_norm_grad_k<T, 8, 0>(p, grid, r.threads, st, device);
-  }
-  if (r.E == 8) return launch_norm_grad_k<T, 1, 8>(p, grid, r.threads, st, device);
-  if (r.E == 16) return launch_norm_grad_k<T, 1, 16>(p, grid, r.threads, st, device);
-  if (r.E == 32) return launch_norm_grad_k<T, 1, 32>(p, grid, r.threads, st, device);
-  return launch_norm_grad_k<T, 1, 0>(p, grid, r.threads, st, device);
+  return with_shape(r, [&](auto V, auto K, auto FULL) {
+    auto kernel = q8::norm_grad_kernel<T, decltype(V)::value, decltype(K)::value, decltype(FULL)::value>;
+    const size_t smem = K > 0 ? 0 : sizeof(float) * size_t(p.d);
+    static bool attr[64] = {false};
+    const cudaError_t e = allow_smem(kernel, smem, &attr[device & 63]);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, r.threads, smem, st>>>(p);
+    return cudaGetLastError();
+  });
 }
 
 template <typename T>
-cudaError_t launch_checkpoint(bool save, const void* src, int8_t* codes, uint8_t* exps, void* dst, int64_t T_, int d,
-                              cudaStream_t st, int device) {
-  const int V = d % 8 == 0 ? 8 : 1;
-  const int64_t warps = T_ * ((d + 32 * V - 1) / (32 * V));
-  int64_t grid = (warps + 7) / 8;
-  const int64_t cap = int64_t(sm_count(device)) * 8;
-  if (grid > cap) grid = cap;
-  const int g = static_cast<int>(grid);
-  if (save) {
-    if (V == 8) q8::checkpoint_save_kernel<T, 8><<<g, 256, 0, st>>>(static_cast<const T*>(src), T_, d, codes, exps);
-    else q8::checkpoint_save_kernel<T, 1><<<g, 256, 0, st>>>(static_cast<const T*>(src), T_, d, codes, exps);
-  } else {
-    if (V == 8) q8::checkpoint_load_kernel<T, 8><<<g, 256, 0, st>>>(codes, exps, T_, d, static_cast<T*>(dst));
-    else q8::checkpoint_load_kernel<T, 1><<<g, 256, 0, st>>>(codes, exps, T_, d, static_cast<T*>(dst));
-  }
-  return cudaGetLastError();
+cudaError_t launch_save(const void* x, int64_t rows, int d, int8_t* codes, uint8_t* exps, cudaStream_t st, int device) {
+  return with_chunks<T, true>(rows, d, device, [&](auto N, dim3 grid) {
+    if constexpr (!(sizeof(T) == 2 && decltype(N)::value == 4))
+      q8::checkpoint_save_kernel<T, decltype(N)::value><<<grid, 128, 0, st>>>(static_cast<const T*>(x), rows, d, codes,
+                                                                              exps);
+    return cudaGetLastError();
+  });
 }
 
 cudaError_t checkpoint_save(int64_t T, int32_t d, const void* x, int32_t dtype, int8_t* codes, uint8_t* exps,
                             cudaStream_t st, int device) {
   PROFILED(ST_CKPT, st,
-           POETX_CUDA_ERR(dtype == POETX_BF16
-                              ? launch_checkpoint<__nv_bfloat16>(true, x, codes, exps, nullptr, T, d, st, device)
-                              : launch_checkpoint<float>(true, x, codes, exps, nullptr, T, d, st, device)));
+           POETX_CUDA_ERR(dtype == POETX_BF16 ? launch_save<__nv_bfloat16>(x, T, d, codes, exps, st, device)
+                                              : launch_save<float>(x, T, d, codes, exps, st, device)));
   return cudaSuccess;
 }
 
 cudaError_t checkpoint_load(int64_t T, int32_t d, const int8_t* codes, const uint8_t* exps, int32_t dtype, void* x,
                             cudaStream_t st, int device) {
-  int8_t* c = const_cast<int8_t*>(codes);
-  uint8_t* e = const_cast<uint8_t*>(exps);
   PROFILED(ST_CKPT, st,
-           POETX_CUDA_ERR(dtype == POETX_BF16 ? launch_checkpoint<__nv_bfloat16>(false, nullptr, c, e, x, T, d, st, device)
-                                              : launch_checkpoint<float>(false, nullptr, c, e, x, T, d, st, device)));
+           POETX_CUDA_ERR(dtype == POETX_BF16
+                              ? launch_expand<__nv_bfloat16>(codes, exps, nullptr, T, d, x, st, device)
+                              : launch_expand<float>(codes, exps, nullptr, T, d, x, st, device)));
   return cudaSuccess;
 }
 
@@ -2039,30 +2085,39 @@ cudaError_t launch_pair_i8(const ProductI8& q, cudaStream_t st, int device) {
   return cudaGetLastError();
 }
 
+// Tiles of the wide kernel, or nt = 0 where the pair kernel is the faster one.
+// Up to 64 tokens take the narrowest tile that holds them.  Beyond, a tile of
+// 64 tokens as long as two CTAs a SM hold them all, then one of 128, then the
+// pair kernel; in us (64, 128, pair), product of T tokens by [n][m]:
+//   333 x 4096 -> 1024:  12, 14, 24     512 x 4096 -> 4096:  18, 20, 26
+//   1024 x 4096 -> 4096: 28, 23, 26     256 x 4096 -> 14336: 27, 24, 28
+//   512 x 4096 -> 14336: 50, 44, 40     1111 x 5120 -> 13824: 118, 99, 68
+// K is split over 2, 4 or 8 CTAs while they all stay resident (four narrow
+// CTAs a SM, else two, and not where the tiles alone fill half the SMs: 200 x
+// 4096 -> 4096 takes 16 us whole, 17 in two); 3, 5 or 6 fit the GPCs badly (1 x
+// 4096 -> 14336: 13.2 us for four, 15.2 for five).
 WideShape wide_shape(int T, int N, int K, int device) {
-  WideShape w;
-  w.nt = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : 256;
-  const int per_sm = w.nt <= 32 ? 4 : w.nt <= 128 ? 2 : 1;   // CTAs an SM holds
-  w.stages = w.nt <= 32 ? (w.nt == 16 ? 3 : 2) : w.nt == 64 ? 4 : w.nt == 128 ? 3 : 4;
-  const int64_t tiles = int64_t((N + 127) / 128) * ((T + w.nt - 1) / w.nt);
+  WideShape w{0, 1, 0};
+  const int sms = sm_count(device);
+  auto tiles_of = [&](int nt) { return int64_t((N + 127) / 128) * ((T + nt - 1) / nt); };
+  w.nt = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 || tiles_of(64) <= 2 * sms ? 64 : T <= 128 || tiles_of(128) <= 2 * sms ? 128 : 0;
+  if (w.nt == 0) return w;
+  const int64_t tiles = tiles_of(w.nt);
   const int nkb = (K + i8::KB - 1) / i8::KB;
-  int64_t S = int64_t(sm_count(device)) * per_sm / tiles;
-  if (S > nkb / 2) S = nkb / 2;
-  if (S > 8) S = 8;
-  w.S = S < 1 ? 1 : static_cast<int>(S);
+  const int64_t slots = w.nt <= 32 ? 4 * sms : tiles <= sms / 2 ? 2 * sms : 0;
+  while (w.S < 8 && 2 * w.S * tiles <= slots && 4 * w.S <= nkb) w.S *= 2;
+  const int64_t per = (tiles * w.S + sms - 1) / sms;  // CTAs a SM
+  const int per_sm = per > (w.nt <= 32 ? 4 : 2) ? (w.nt <= 32 ? 4 : 2) : static_cast<int>(per);
+  const int stage = i8::BOX_BYTES + w.nt * i8::KB;
+  w.stages = (228 * 1024 / per_sm - 1024 - 1280) / stage;  // 1 KB of the SM's 228 goes to the system for each CTA
+  if (w.stages > 8) w.stages = 8;
   return w;
 }
 
 cudaError_t product_i8(const ProductI8& q, int32_t dtype, cudaStream_t st, int device) {
-  const int64_t tiles = int64_t((q.T + 255) / 256) * ((q.N + 255) / 256);
-  bool pair = q.T > 256 && 2 * tiles >= sm_count(device);
-  WideShape w = wide_shape(q.T, q.N, q.K, device);
-#ifdef TUNE
-  if (const char* e = getenv("I8P")) pair = atoi(e);
-  if (const char* e = getenv("I8W")) sscanf(e, "%d,%d,%d", &w.nt, &w.S, &w.stages);
-#endif
+  const WideShape w = wide_shape(q.T, q.N, q.K, device);
   Prof prof(ST_INT8, st);
-  if (pair)
+  if (w.nt == 0)
     return dtype == POETX_BF16 ? launch_pair_i8<__nv_bfloat16>(q, st, device) : launch_pair_i8<float>(q, st, device);
   return dtype == POETX_BF16 ? launch_wide_i8<__nv_bfloat16>(q, w, st, device) : launch_wide_i8<float>(q, w, st, device);
 }
@@ -2146,9 +2201,9 @@ poetx_status poetx_rmsnorm_quantize(int64_t T, int32_t d, const void* x, const v
   return POETX_OK;
 }
 
-size_t poetx_rmsnorm_backward_workspace_bytes(int64_t T, int32_t d) {
-  if (check_rows(T, d, kMaxM) != POETX_OK) return 0;
-  return kAlign + al(sizeof(float) * size_t(norm_grad_grid(T, row_shape(d).threads)) * d);
+size_t poetx_rmsnorm_backward_workspace_bytes(int64_t T, int32_t d, int32_t dtype) {
+  if (check_dtype(dtype) != POETX_OK || check_rows(T, d, kMaxM) != POETX_OK) return 0;
+  return kAlign + al(sizeof(float) * size_t(norm_grad_grid(T, norm_grad_shape(d, dtype).threads)) * d);
 }
 
 poetx_status poetx_rmsnorm_backward(int64_t T, int32_t d, const void* dy, const void* h, const float* gamma,
@@ -2165,10 +2220,10 @@ poetx_status poetx_rmsnorm_backward(int64_t T, int32_t d, const void* dy, const 
   const void* need[] = {dy, h, gamma, rstd, dx};
   for (const void* p : need) POETX_TRY(check_ptr(p));
   POETX_TRY(check_opt(dres));
-  if (!ws || ws_bytes < poetx_rmsnorm_backward_workspace_bytes(T, d)) return POETX_E_WORKSPACE;
+  if (!ws || ws_bytes < poetx_rmsnorm_backward_workspace_bytes(T, d, dtype)) return POETX_E_WORKSPACE;
   int dev;
   POETX_TRY(current_device(&dev));
-  const RowShape r = row_shape(d);
+  const RowShape r = norm_grad_shape(d, dtype);
   const int grid = norm_grad_grid(T, r.threads);
   Carver c(ws, ws_bytes);
   q8::NormGradParams p;

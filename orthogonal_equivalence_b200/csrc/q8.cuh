@@ -5,11 +5,12 @@
 // outputs once, so HBM bandwidth is their floor.
 //
 // Quantised rows.  For a row u (fp32): scale = max|u| / 127 (fp32 division),
-// code = u / scale rounded half to even.  The quotient is never formed: with
-// q = round(u * (1 / scale)) the remainder r = u - q * scale is exact (it is a
-// multiple of ulp(scale) no larger than scale in magnitude, one FMA), and
-// 2|r| < scale proves q; the rare other lanes step q by one.  So the codes are
-// those of the real quotient, whatever the order of any reduction.
+// code = u / scale rounded half to even.  The quotient is never formed: it is
+// bracketed by u times two bounds of 1 / scale, and where the brackets round
+// apart, the remainder r = u - q * scale of q = round(u * (1 / scale)) decides;
+// it is exact (a multiple of ulp(scale) no larger than scale in magnitude, one
+// FMA).  So the codes are those of the real quotient, whatever the order of
+// any reduction.
 // A row that holds an infinity or a NaN gets codes 0 and scale NaN, so it
 // cannot pass for an ordinary row; a row of zeros gets codes 0 and scale 0.
 #pragma once
@@ -23,19 +24,54 @@
 namespace poetx {
 namespace q8 {
 
+constexpr int kRowThreads = 448;   // most threads of a row's block: two blocks of 72 registers fit a SM
+
 // ---------------------------------------------------------------- loads and stores
-// V consecutive elements as fp32 (V = 8: 16-byte vectors; V = 1: one element).
+// Eight elements of a row of d as loaded: consecutive ones from c (V = 8,
+// whole 16-byte vectors), or c, c + nt, ... (V = 1, any row).  Behind the
+// row's end: zeros.  FULL: the block's threads cover the row exactly, nothing
+// to check.
 template <typename T, int V>
-__device__ __forceinline__ void load_vec(const T* p, float* f) {
+struct Raw8 {
+  T v[8];
+};
+template <>
+struct Raw8<__nv_bfloat16, 8> {
+  uint4 v;
+};
+template <>
+struct Raw8<float, 8> {
+  float4 v[2];
+};
+
+template <typename T, int V, bool FULL>
+__device__ __forceinline__ void fetch8(Raw8<T, V>& r, const T* p, int c, int nt, int d) {
   if constexpr (V == 1) {
-    f[0] = to_f32<T>(*p);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r.v[e] = c + e * nt < d ? p[c + e * nt] : from_f32<T>(0.f);
   } else if constexpr (std::is_same<T, float>::value) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    const bool in = FULL || c < d;
+    r.v[0] = in ? reinterpret_cast<const float4*>(p + c)[0] : make_float4(0.f, 0.f, 0.f, 0.f);
+    r.v[1] = in ? reinterpret_cast<const float4*>(p + c)[1] : make_float4(0.f, 0.f, 0.f, 0.f);
   } else {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+    r.v = FULL || c < d ? *reinterpret_cast<const uint4*>(p + c) : make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void unpack8(const Raw8<T, V>& r, float* f) {
+  if constexpr (V == 1) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = to_f32<T>(r.v[e]);
+  } else if constexpr (std::is_same<T, float>::value) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f[4 * i] = r.v[i].x;
+      f[4 * i + 1] = r.v[i].y;
+      f[4 * i + 2] = r.v[i].z;
+      f[4 * i + 3] = r.v[i].w;
+    }
+  } else {
+    const uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       f[2 * i] = __uint_as_float(w[i] << 16);
@@ -43,87 +79,118 @@ __device__ __forceinline__ void load_vec(const T* p, float* f) {
     }
   }
 }
-
+// f rounded to T, as loaded.
 template <typename T, int V>
-__device__ __forceinline__ void store_vec(T* p, const float* f) {
+__device__ __forceinline__ void pack8(Raw8<T, V>& r, const float* f) {
   if constexpr (V == 1) {
-    *p = from_f32<T>(f[0]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r.v[e] = from_f32<T>(f[e]);
   } else if constexpr (std::is_same<T, float>::value) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    r.v[0] = make_float4(f[0], f[1], f[2], f[3]);
+    r.v[1] = make_float4(f[4], f[5], f[6], f[7]);
   } else {
-    uint4 a;
-    uint32_t* w = reinterpret_cast<uint32_t*>(&a);
+    uint32_t* w = reinterpret_cast<uint32_t*>(&r.v);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
       w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    *reinterpret_cast<uint4*>(p) = a;
   }
 }
-
-// f rounded to T and back.
-template <typename T>
-__device__ __forceinline__ float round_to(float f) {
-  return to_f32<T>(from_f32<T>(f));
+template <typename T, int V, bool FULL>
+__device__ __forceinline__ void put8(T* p, int c, int nt, int d, const Raw8<T, V>& r) {
+  if constexpr (V == 1) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c + e * nt < d) p[c + e * nt] = r.v[e];
+  } else if (FULL || c < d) {
+    if constexpr (std::is_same<T, float>::value) {
+      reinterpret_cast<float4*>(p + c)[0] = r.v[0];
+      reinterpret_cast<float4*>(p + c)[1] = r.v[1];
+    } else {
+      *reinterpret_cast<uint4*>(p + c) = r.v;
+    }
+  }
+}
+template <typename T, int V, bool FULL>
+__device__ __forceinline__ void load8(const T* p, int c, int nt, int d, float* f) {
+  Raw8<T, V> r;
+  fetch8<T, V, FULL>(r, p, c, nt, d);
+  unpack8<T, V>(r, f);
+}
+template <typename T, int V, bool FULL>
+__device__ __forceinline__ void store8(T* p, int c, int nt, int d, const float* f) {
+  Raw8<T, V> r;
+  pack8<T, V>(r, f);
+  put8<T, V, FULL>(p, c, nt, d, r);
 }
 
 // ---------------------------------------------------------------- quantiser
 constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds half to even, low byte = the integer
 
 struct RowScale {
-  float s, inv;
+  float s, inv, lo, hi;  // inv ~ 1 / s, lo < 1 / s < hi
   int kind;  // 0: zero row, 1: ordinary, 2: scale too small for 1 / s, 3: not finite
 };
 
 __device__ __forceinline__ RowScale row_scale(float amax) {
   RowScale r;
   r.s = amax / 127.f;
-  r.inv = 1.f / r.s;
+  r.inv = __fdividef(1.f, r.s);       // good to a few units in the last place (2^-24 each)
+  r.lo = r.inv * (1.f - 0x1p-20f);
+  r.hi = r.inv * (1.f + 0x1p-20f);
   r.kind = !(amax <= 3.402823466e38f) ? 3 : !(r.s > 0.f) ? 0 : r.s < 1e-36f ? 2 : 1;
   if (r.kind == 3) r.s = __uint_as_float(0x7fffffffu);
   return r;
 }
 
-__device__ __forceinline__ int quantise_far(float u, const RowScale& r) {
-  if (r.kind != 2) return 0;
+// One code, slowly: rows whose scale is too small to invert (its own quotient
+// in 64 bits), zero and non-finite rows.
+__device__ __forceinline__ uint32_t quantise_far(float u, const RowScale& r) {
+  if (r.kind != 2) return 0u;
   const double q = rint(static_cast<double>(u) / static_cast<double>(r.s));
-  return static_cast<int>(fmin(fmax(q, -127.0), 127.0));
+  return static_cast<uint32_t>(static_cast<int>(fmin(fmax(q, -127.0), 127.0))) & 0xffu;
 }
 
-__device__ __forceinline__ int quantise(float u, const RowScale& r) {
-  const float m = fmaf(u, r.inv, kMagic);
-  float q = m - kMagic;
-  const float rem = fmaf(-q, r.s, u);
-  const float twice = 2.f * fabsf(rem);
-  int code = __float_as_int(m) & 0xff;
-  if (!(twice < r.s)) {  // a border: the nearest code, the even one on a tie
-    const float step = copysignf(1.f, rem);
-    const int qi = static_cast<int>(q);
-    if (twice > r.s || (qi & 1)) code = (qi + static_cast<int>(step)) & 0xff;
-  }
-  return code;
+// One code at a border: the nearest, the even one on a tie.
+__device__ __forceinline__ uint32_t quantise_border(float u, const RowScale& r) {
+  const float m = fmaf(u, r.inv, kMagic), q = m - kMagic;
+  const float rem = fmaf(-q, r.s, u), twice = 2.f * fabsf(rem);
+  int c = static_cast<int>(q);
+  if (twice > r.s || (twice == r.s && (c & 1))) c += rem > 0.f ? 1 : -1;
+  return static_cast<uint32_t>(c) & 0xffu;
 }
 
-// V codes of V values.
-template <int V>
-__device__ __forceinline__ void store_codes(int8_t* p, const float* u, const RowScale& r) {
-  int c[V];
+// The codes of eight values (placed as in load8).  The quotient lies between
+// u * lo and u * hi; where both round to the same integer that is the code
+// (two FMAs a value, one branch for all eight).
+template <int V, bool FULL>
+__device__ __forceinline__ void store_codes(int8_t* p, int c, int nt, int d, const float* u, const RowScale& r) {
+  uint32_t q[8];
   if (r.kind == 1) {
+    uint32_t differ = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) c[i] = quantise(u[i], r);
+    for (int i = 0; i < 8; ++i) {
+      q[i] = __float_as_uint(fmaf(u[i], r.lo, kMagic));
+      differ |= q[i] ^ __float_as_uint(fmaf(u[i], r.hi, kMagic));
+    }
+    if (differ) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i] = quantise_border(u[i], r);
+    }
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) c[i] = quantise_far(u[i], r);
+    for (int i = 0; i < 8; ++i) q[i] = quantise_far(u[i], r);
   }
   if constexpr (V == 1) {
-    *p = static_cast<int8_t>(c[0]);
-  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i * nt < d) p[c + i * nt] = static_cast<int8_t>(q[i]);
+  } else if (FULL || c < d) {
     uint2 w;
-    w.x = (c[0] & 0xff) | (c[1] & 0xff) << 8 | (c[2] & 0xff) << 16 | (c[3] & 0xff) << 24;
-    w.y = (c[4] & 0xff) | (c[5] & 0xff) << 8 | (c[6] & 0xff) << 16 | (c[7] & 0xff) << 24;
-    *reinterpret_cast<uint2*>(p) = w;
+    w.x = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+    w.y = __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410);
+    *reinterpret_cast<uint2*>(p + c) = w;
   }
 }
 
@@ -134,27 +201,46 @@ __device__ __forceinline__ float nan_max(float a, float b) {
   return r;
 }
 
-// Sum of `a` and maximum of `b` over the block; red holds 2 * 32 floats and is
-// free again after the next call's barrier (callers alternate two of them).
-__device__ __forceinline__ void block_sum_max(float& a, float& b, float* red) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, o);
-    b = nan_max(b, __shfl_xor_sync(0xffffffffu, b, o));
-  }
-  const int nw = blockDim.x >> 5, w = threadIdx.x >> 5, l = threadIdx.x & 31;
-  if (l == 0) {
-    red[w] = a;
-    red[32 + w] = b;
+// Sum of `a` (SUM) and maximum of `b` >= 0 (MAX, a NaN stays one) over a block
+// of at most 16 warps; red holds 2 * 16 floats, zero beyond the block's warps,
+// and is free again after the next call's barrier (callers alternate two).
+struct alignas(16) BlockSums {
+  float sum[16], top[16];
+};
+__device__ __forceinline__ void clear_sums(BlockSums* r) {
+  if (threadIdx.x < 32) {
+    for (int b = 0; b < 2; ++b) (threadIdx.x < 16 ? r[b].sum : r[b].top)[threadIdx.x & 15] = 0.f;
   }
   __syncthreads();
-  a = l < nw ? red[l] : 0.f;
-  b = l < nw ? red[32 + l] : 0.f;
+}
+template <bool SUM, bool MAX>
+__device__ __forceinline__ void block_reduce(float& a, float& b, BlockSums* red) {
+  if (SUM) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, o);
-    b = nan_max(b, __shfl_xor_sync(0xffffffffu, b, o));
+    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
   }
+  // bits of non-negative floats are ordered as the floats, NaN above infinity
+  if (MAX) b = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(b) & 0x7fffffffu));
+  const int w = threadIdx.x >> 5;
+  if ((threadIdx.x & 31) == 0) {
+    if (SUM) red->sum[w] = a;
+    if (MAX) red->top[w] = b;
+  }
+  __syncthreads();
+  const int n4 = (blockDim.x + 127) >> 7;  // groups of four warps
+  float s = 0.f, t = 0.f;
+  for (int i = 0; i < n4; ++i) {
+    if (SUM) {
+      const float4 v = reinterpret_cast<const float4*>(red->sum)[i];
+      s += (v.x + v.y) + (v.z + v.w);
+    }
+    if (MAX) {
+      const float4 v = reinterpret_cast<const float4*>(red->top)[i];
+      t = nan_max(t, nan_max(nan_max(v.x, v.y), nan_max(v.z, v.w)));
+    }
+  }
+  a = s;
+  b = t;
 }
 
 // ---------------------------------------------------------------- rows to int8, with or without the norm
@@ -177,95 +263,106 @@ struct RowsParams {
 // rounded to T, rstd = 1 / sqrt(mean h^2 + eps), u = h * gamma; else u = x or
 // x * gain.  The codes of u and of rstd * u are the same (the factor cancels
 // in u / max|u|), so one reduction gives both the sum of squares and the
-// maximum, and the row is read once: thread t holds elements
-// (t + k * blockDim) * V + e for k < K in registers.  K = 0: rows too wide
-// for that are read a second time (h as written; each thread rereads only
-// what it wrote itself).
-template <typename T, bool NORM, int V, int K>
-__global__ void __launch_bounds__(512) rows_kernel(const RowsParams p) {
-  __shared__ float red[2][64];
+// maximum, and the row is read once: a thread holds K times eight elements in
+// registers, and loads its next row's before it works on this one.  K = 0:
+// rows too wide for registers are read a second time (h as written; each
+// thread rereads only what it wrote itself).
+template <typename T, bool NORM, int V, int K, bool FULL>
+__global__ void __launch_bounds__(NORM && K == 2 && V == 8 ? 512 : kRowThreads, NORM && (K == 4 || V == 1) ? 1 : 2)
+    rows_kernel(const RowsParams p) {
+  __shared__ BlockSums red[2];
   const T* xs = static_cast<const T*>(p.x);
   const T* rs = static_cast<const T*>(p.residual);
   T* hs = static_cast<T*>(p.h);
   T* ys = static_cast<T*>(p.y);
   constexpr int KR = K > 0 ? K : 1;
-  const int step = blockDim.x * V, first = threadIdx.x * V;
+  const int nt = blockDim.x, first = threadIdx.x * V, step = nt * 8, d = p.d;
+  const bool gain = NORM || p.gain;
+  clear_sums(red);
+  Raw8<T, V> nx[KR], nr[NORM ? KR : 1];
+  auto fetch = [&](int64_t row) {
+#pragma unroll
+    for (int k = 0; k < KR; ++k) fetch8<T, V, FULL>(nx[k], xs + row * d, first + k * step, nt, d);
+    if (NORM && rs) {
+#pragma unroll
+      for (int k = 0; k < KR; ++k) fetch8<T, V, FULL>(nr[NORM ? k : 0], rs + row * d, first + k * step, nt, d);
+    }
+  };
+  if (K > 0 && blockIdx.x < p.T) fetch(blockIdx.x);
   int buf = 0;
   for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x, buf ^= 1) {
-    const int64_t base = row * p.d;
-    float u[KR][V];
+    const int64_t base = row * d;
+    float u[KR][8];
     float sum = 0.f, top = 0.f;
-    auto element = [&](int c, float* v) {
-      load_vec<T, V>(xs + base + c, v);
+    // h (u so far) from x and the residual
+    auto summed = [&](int c, float* v, const Raw8<T, V>& r) {
       if constexpr (NORM) {
         if (rs) {
-          float r[V];
-          load_vec<T, V>(rs + base + c, r);
+          float f[8];
+          unpack8<T, V>(r, f);
 #pragma unroll
-          for (int e = 0; e < V; ++e) v[e] = round_to<T>(v[e] + r[e]);
+          for (int e = 0; e < 8; ++e) v[e] += f[e];
+          Raw8<T, V> h;
+          pack8<T, V>(h, v);
+          if (hs) put8<T, V, FULL>(hs + base, c, nt, d, h);
+          unpack8<T, V>(h, v);
+        } else if (hs) {
+          store8<T, V, FULL>(hs + base, c, nt, d, v);
         }
-        if (hs) store_vec<T, V>(hs + base + c, v);
 #pragma unroll
-        for (int e = 0; e < V; ++e) sum = fmaf(v[e], v[e], sum);
+        for (int e = 0; e < 8; ++e) sum = fmaf(v[e], v[e], sum);
       }
     };
     auto gained = [&](int c, float* v) {
-      if (NORM || p.gain) {
-        float g[V];
-        load_vec<float, V>(p.gain + c, g);
+      if (gain) {
+        float g[8];
+        load8<float, V, FULL>(p.gain, c, nt, d, g);
 #pragma unroll
-        for (int e = 0; e < V; ++e) v[e] *= g[e];
+        for (int e = 0; e < 8; ++e) v[e] *= g[e];
       }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = nan_max(top, fabsf(v[e]));
     };
     if constexpr (K > 0) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        const int c = first + k * step;
-        if (c < p.d) element(c, u[k]);
+        unpack8<T, V>(nx[k], u[k]);
+        summed(first + k * step, u[k], nr[NORM ? k : 0]);
       }
+      if (row + gridDim.x < p.T) fetch(row + gridDim.x);
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int c = first + k * step;
-        if (c < p.d) {
-          gained(c, u[k]);
-#pragma unroll
-          for (int e = 0; e < V; ++e) top = nan_max(top, fabsf(u[k][e]));
-        }
-      }
+      for (int k = 0; k < K; ++k) gained(first + k * step, u[k]);
     } else {
-      for (int c = first; c < p.d; c += step) {
-        element(c, u[0]);
+      for (int c = first; c < d; c += step) {
+        load8<T, V, FULL>(xs + base, c, nt, d, u[0]);
+        if (NORM && rs) fetch8<T, V, FULL>(nr[0], rs + base, c, nt, d);
+        summed(c, u[0], nr[0]);
         gained(c, u[0]);
-#pragma unroll
-        for (int e = 0; e < V; ++e) top = nan_max(top, fabsf(u[0][e]));
       }
     }
-    block_sum_max(sum, top, red[buf]);
+    block_reduce<NORM, true>(sum, top, &red[buf]);
     const RowScale sc = row_scale(top);
     float rstd = 1.f;
-    if constexpr (NORM) rstd = 1.f / sqrtf(sum / static_cast<float>(p.d) + p.eps);
+    if constexpr (NORM) rstd = rsqrtf(sum / static_cast<float>(d) + p.eps);
     if (threadIdx.x == 0) {
       if (p.codes) p.scale[row] = sc.s * rstd;
       if (NORM && p.rstd) p.rstd[row] = rstd;
     }
     auto finish = [&](int c, float* v) {
-      if (p.codes) store_codes<V>(p.codes + row * p.ldc + c, v, sc);
+      if (p.codes) store_codes<V, FULL>(p.codes + row * p.ldc, c, nt, d, v, sc);
       if (NORM && ys) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) v[e] *= rstd;
-        store_vec<T, V>(ys + base + c, v);
+        for (int e = 0; e < 8; ++e) v[e] *= rstd;
+        store8<T, V, FULL>(ys + base, c, nt, d, v);
       }
     };
     if constexpr (K > 0) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int c = first + k * step;
-        if (c < p.d) finish(c, u[k]);
-      }
+      for (int k = 0; k < K; ++k) finish(first + k * step, u[k]);
     } else {
-      const T* again = NORM && hs ? hs : xs;
-      for (int c = first; c < p.d; c += step) {
-        load_vec<T, V>(again + base + c, u[0]);
+      const T* again = NORM && hs ? hs + base : xs + base;
+      for (int c = first; c < d; c += step) {
+        load8<T, V, FULL>(again, c, nt, d, u[0]);
         gained(c, u[0]);
         finish(c, u[0]);
       }
@@ -291,38 +388,46 @@ struct NormGradParams {
 // blockIdx.x + gridDim.x, ...; a thread keeps its columns' share of dgamma in
 // registers over all of them (K > 0) or in its own words of shared memory
 // (K = 0, any width), so the sum's order is fixed by the grid alone.
-template <typename T, int V, int K>
-__global__ void __launch_bounds__(512) norm_grad_kernel(const NormGradParams p) {
-  extern __shared__ float acc_sm[];
-  __shared__ float red[2][64];
+template <typename T, int V, int K, bool FULL>
+__global__ void __launch_bounds__(kRowThreads) norm_grad_kernel(const NormGradParams p) {
+  extern __shared__ float acc_sm[];  // K = 0
+  __shared__ BlockSums red[2];
   const T* dys = static_cast<const T*>(p.dy);
   const T* hs = static_cast<const T*>(p.h);
   const T* rs = static_cast<const T*>(p.dres);
   T* dxs = static_cast<T*>(p.dx);
   constexpr int KR = K > 0 ? K : 1;
-  const int step = blockDim.x * V, first = threadIdx.x * V;
-  float acc[KR][V];
-  if constexpr (K > 0) {
+  const int nt = blockDim.x, first = threadIdx.x * V, step = nt * 8, d = p.d;
+  float acc[KR][8];
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+  for (int k = 0; k < KR; ++k)
 #pragma unroll
-      for (int e = 0; e < V; ++e) acc[k][e] = 0.f;
-  } else {
-    for (int c = first; c < p.d; c += step)
+    for (int e = 0; e < 8; ++e) acc[k][e] = 0.f;
+  if constexpr (K == 0)
+    for (int c = first; c < d; c += step) store8<float, V, FULL>(acc_sm, c, nt, d, acc[0]);
+  clear_sums(red);
+  Raw8<T, V> ny[KR], nh[KR], nr[KR];
+  float next_rstd = 0.f;
+  auto fetch = [&](int64_t row) {
+    next_rstd = p.rstd[row];
 #pragma unroll
-      for (int e = 0; e < V; ++e) acc_sm[c + e] = 0.f;
-  }
+    for (int k = 0; k < KR; ++k) {
+      fetch8<T, V, FULL>(ny[k], dys + row * d, first + k * step, nt, d);
+      fetch8<T, V, FULL>(nh[k], hs + row * d, first + k * step, nt, d);
+    }
+  };
+  if (K > 0 && blockIdx.x < p.T) fetch(blockIdx.x);
   int buf = 0;
   for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x, buf ^= 1) {
-    const int64_t base = row * p.d;
-    const float rstd = p.rstd[row];
+    const int64_t base = row * d;
     float dot = 0.f, none = 0.f;
-    float dy[KR][V], h[KR][V];
+    float dy[KR][8], h[KR][8];
+    const float rstd = K > 0 ? next_rstd : p.rstd[row];
     auto dots = [&](int c, float* a, float* b, float* w) {
-      float g[V];
-      load_vec<float, V>(p.gamma + c, g);
+      float g[8];
+      load8<float, V, FULL>(p.gamma, c, nt, d, g);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
+      for (int e = 0; e < 8; ++e) {
         b[e] *= rstd;
         w[e] = fmaf(a[e], b[e], w[e]);
         a[e] *= g[e];
@@ -332,66 +437,62 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(const NormGradParams p) 
     if constexpr (K > 0) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        const int c = first + k * step;
-        if (c < p.d) {
-          load_vec<T, V>(dys + base + c, dy[k]);
-          load_vec<T, V>(hs + base + c, h[k]);
-        }
+        unpack8<T, V>(ny[k], dy[k]);
+        unpack8<T, V>(nh[k], h[k]);
+        if (rs) fetch8<T, V, FULL>(nr[k], rs + base, first + k * step, nt, d);
       }
+      if (row + gridDim.x < p.T) fetch(row + gridDim.x);
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int c = first + k * step;
-        if (c < p.d) dots(c, dy[k], h[k], acc[k]);
-      }
+      for (int k = 0; k < K; ++k) dots(first + k * step, dy[k], h[k], acc[k]);
     } else {
-      for (int c = first; c < p.d; c += step) {
-        load_vec<T, V>(dys + base + c, dy[0]);
-        load_vec<T, V>(hs + base + c, h[0]);
-        dots(c, dy[0], h[0], acc_sm + c);
+      for (int c = first; c < d; c += step) {
+        load8<T, V, FULL>(dys + base, c, nt, d, dy[0]);
+        load8<T, V, FULL>(hs + base, c, nt, d, h[0]);
+        load8<float, V, FULL>(acc_sm, c, nt, d, acc[0]);
+        dots(c, dy[0], h[0], acc[0]);
+        store8<float, V, FULL>(acc_sm, c, nt, d, acc[0]);
       }
     }
-    block_sum_max(dot, none, red[buf]);
-    const float mean = dot / static_cast<float>(p.d);
-    auto finish = [&](int c, const float* a, const float* b) {
-      float o[V];
-      if (rs) load_vec<T, V>(rs + base + c, o);
+    block_reduce<true, false>(dot, none, &red[buf]);
+    const float mean = dot / static_cast<float>(d);
+    auto finish = [&](int c, const float* a, const float* b, const Raw8<T, V>& res) {
+      float o[8], r[8];
+      if (rs) unpack8<T, V>(res, r);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
+      for (int e = 0; e < 8; ++e) {
         const float v = fmaf(-b[e], mean, a[e]);
-        o[e] = rs ? fmaf(rstd, v, o[e]) : rstd * v;
+        o[e] = rs ? fmaf(rstd, v, r[e]) : rstd * v;
       }
-      store_vec<T, V>(dxs + base + c, o);
+      store8<T, V, FULL>(dxs + base, c, nt, d, o);
     };
     if constexpr (K > 0) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int c = first + k * step;
-        if (c < p.d) finish(c, dy[k], h[k]);
-      }
+      for (int k = 0; k < K; ++k) finish(first + k * step, dy[k], h[k], nr[k]);
     } else {
-      for (int c = first; c < p.d; c += step) {
-        float g[V];
-        load_vec<T, V>(dys + base + c, dy[0]);
-        load_vec<T, V>(hs + base + c, h[0]);
-        load_vec<float, V>(p.gamma + c, g);
+      for (int c = first; c < d; c += step) {
+        float g[8];
+        load8<T, V, FULL>(dys + base, c, nt, d, dy[0]);
+        load8<T, V, FULL>(hs + base, c, nt, d, h[0]);
+        load8<float, V, FULL>(p.gamma, c, nt, d, g);
+        if (rs) fetch8<T, V, FULL>(nr[0], rs + base, c, nt, d);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
+        for (int e = 0; e < 8; ++e) {
           dy[0][e] *= g[e];
           h[0][e] *= rstd;
         }
-        finish(c, dy[0], h[0]);
+        finish(c, dy[0], h[0], nr[0]);
       }
     }
   }
-  float* out = p.part + static_cast<int64_t>(blockIdx.x) * p.d;
+  float* out = p.part + static_cast<int64_t>(blockIdx.x) * d;
   if constexpr (K > 0) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = first + k * step;
-      if (c < p.d) store_vec<float, V>(out + c, acc[k]);
-    }
+    for (int k = 0; k < K; ++k) store8<float, V, FULL>(out, first + k * step, nt, d, acc[k]);
   } else {
-    for (int c = first; c < p.d; c += step) store_vec<float, V>(out + c, acc_sm + c);
+    for (int c = first; c < d; c += step) {
+      load8<float, V, FULL>(acc_sm, c, nt, d, acc[0]);
+      store8<float, V, FULL>(out, c, nt, d, acc[0]);
+    }
   }
 }
 
@@ -478,79 +579,166 @@ __device__ __forceinline__ float exponent_value(uint32_t eb) {    // 2^e, NaN fo
 __device__ __forceinline__ uint32_t checkpoint_code(float v, float inv) {
   return inv == 0.f ? 0u : __float_as_uint(fmaf(v, inv, kMagic)) & 0xffu;
 }
+__device__ __forceinline__ float kept(float v) { return copysignf(fminf(fabsf(v), __uint_as_float(kMaxKept)), v); }
 
-// A warp takes 32 * V columns of a row: with V = 8, four lanes hold a group.
-template <typename T, int V>
-__global__ void __launch_bounds__(256) checkpoint_save_kernel(const T* __restrict__ x, int64_t T_, int d,
+// N elements as fp32 in 16-byte units (4 fp32 or 8 bf16 each).
+template <typename T, int N>
+__device__ __forceinline__ void load_units(const T* p, float* f) {
+  if constexpr (std::is_same<T, float>::value) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const float4 a = reinterpret_cast<const float4*>(p)[i];
+      f[4 * i] = a.x;
+      f[4 * i + 1] = a.y;
+      f[4 * i + 2] = a.z;
+      f[4 * i + 3] = a.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i) {
+      Raw8<T, 8> r;
+      fetch8<T, 8, true>(r, p + 8 * i, 0, 0, 0);
+      unpack8<T, 8>(r, f + 8 * i);
+    }
+  }
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_units(T* p, const float* f) {
+  if constexpr (std::is_same<T, float>::value) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i)
+      reinterpret_cast<float4*>(p)[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i) store8<T, 8, true>(p + 8 * i, 0, 0, 0, f + 8 * i);
+  }
+}
+// N int8 codes from or to one word of N bytes (N = 4, 8 or 16).
+template <int N>
+__device__ __forceinline__ void load_codes(const int8_t* p, uint32_t* w) {
+  if constexpr (N == 16) *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p);
+  else if constexpr (N == 8) *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
+  else *w = *reinterpret_cast<const uint32_t*>(p);
+}
+template <int N>
+__device__ __forceinline__ void write_codes(int8_t* p, const uint32_t* w) {
+  if constexpr (N == 16) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(w);
+  else if constexpr (N == 8) *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(w);
+  else *reinterpret_cast<uint32_t*>(p) = *w;
+}
+__device__ __forceinline__ float code_value(const uint32_t* w, int i) {
+  return static_cast<float>(static_cast<int8_t>(w[i >> 2] >> (8 * (i & 3))));
+}
+
+// The kernels below give a warp 32 * N columns of a row, N of them consecutive
+// to a lane (16 or 8 bf16, 8 or 4 fp32), so that a warp's accesses are whole
+// lines: at 16384 x 4096 bf16 saving takes 32 us and reading back 35 us (31 us
+// is the copy rate).  N = 1,
+// for rows that are no whole vectors: a lane takes one column of each of eight
+// groups.  Chunks of rows are walked without a division by the grid's shape:
+// blockIdx.x and the warp give the chunk, blockIdx.y strides over the rows.
+constexpr int kOddGroups = 8;
+template <int N>
+constexpr int chunk_cols = N == 1 ? GROUP * kOddGroups : 32 * N;
+
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+template <typename T, int N>
+__global__ void __launch_bounds__(128) checkpoint_save_kernel(const T* __restrict__ x, int64_t rows, int d,
                                                               int8_t* __restrict__ codes, uint8_t* __restrict__ exps) {
   const int lane = threadIdx.x & 31;
   const int ng = (d + GROUP - 1) / GROUP;
-  const int chunks = (d + 32 * V - 1) / (32 * V);
-  const int64_t items = T_ * chunks;
-  constexpr int LG = GROUP / V;  // lanes of a group
-  const int64_t nw = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
-  for (int64_t it = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); it < items; it += nw) {
-    const int64_t row = it / chunks;
-    const int c = static_cast<int>(it - row * chunks) * 32 * V + lane * V;
-    float v[V];
-    float top = 0.f;
-    if (c < d) {
-      load_vec<T, V>(x + row * d + c, v);
+  const int c0 = (blockIdx.x * 4 + (threadIdx.x >> 5)) * chunk_cols<N>;
+  if (c0 >= d) return;
+  for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
+    if constexpr (N == 1) {
+      const int64_t at = row * d;
+      float v[kOddGroups];
 #pragma unroll
-      for (int e = 0; e < V; ++e) top = nan_max(top, fabsf(v[e]));
-    }
-#pragma unroll
-    for (int o = LG / 2; o > 0; o >>= 1) top = nan_max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (c < d) {
-      const uint32_t eb = group_exponent(top);
-      const float inv = exponent_inverse(eb);
-      if (top > __uint_as_float(kMaxKept)) {
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-          v[e] = copysignf(fminf(fabsf(v[e]), __uint_as_float(kMaxKept)), v[e]);
+      for (int g = 0; g < kOddGroups; ++g) {
+        const int c = c0 + g * GROUP + lane;
+        v[g] = c < d ? to_f32<T>(x[at + c]) : 0.f;
       }
-      if (lane % LG == 0) exps[row * ng + c / GROUP] = static_cast<uint8_t>(eb);
-      if constexpr (V == 1) {
-        codes[row * d + c] = static_cast<int8_t>(checkpoint_code(v[0], inv));
-      } else {
-        uint32_t q[8];
+      uint32_t mine = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) q[e] = checkpoint_code(v[e], inv);
-        uint2 w;
-        w.x = q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24;
-        w.y = q[4] | q[5] << 8 | q[6] << 16 | q[7] << 24;
-        *reinterpret_cast<uint2*>(codes + row * d + c) = w;
+      for (int g = 0; g < kOddGroups; ++g) {
+        const int c = c0 + g * GROUP + lane;
+        const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, magnitude(v[g])));
+        const uint32_t eb = group_exponent(top);
+        if (lane == g) mine = eb;
+        if (c < d) codes[at + c] = static_cast<int8_t>(checkpoint_code(kept(v[g]), exponent_inverse(eb)));
+      }
+      if (lane < kOddGroups && c0 / GROUP + lane < ng) exps[row * ng + c0 / GROUP + lane] = static_cast<uint8_t>(mine);
+    } else {
+      constexpr int LG = GROUP / N;  // lanes of a group
+      const int c = c0 + lane * N;
+      const bool in = c < d;  // (d is a multiple of N)
+      float v[N];
+      uint32_t top = 0;
+      if (in) {
+        load_units<T, N>(x + row * d + c, v);
+#pragma unroll
+        for (int e = 0; e < N; ++e) top = max(top, magnitude(v[e]));
+      }
+#pragma unroll
+      for (int o = LG / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (in) {
+        const uint32_t eb = group_exponent(__uint_as_float(top));
+        const float inv = exponent_inverse(eb);
+        if (top > kMaxKept && eb != 255u) {
+#pragma unroll
+          for (int e = 0; e < N; ++e) v[e] = kept(v[e]);
+        }
+        if (lane % LG == 0) exps[row * ng + c / GROUP] = static_cast<uint8_t>(eb);
+        uint32_t w[N / 4];
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+          uint32_t q[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) q[e] = __float_as_uint(fmaf(v[4 * i + e], inv, kMagic));
+          w[i] = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+          if (eb == 255u) w[i] = 0;
+        }
+        write_codes<N>(codes + row * d + c, w);
       }
     }
   }
 }
 
-template <typename T, int V>
-__global__ void __launch_bounds__(256) checkpoint_load_kernel(const int8_t* __restrict__ codes,
-                                                              const uint8_t* __restrict__ exps, int64_t T_, int d,
-                                                              T* __restrict__ x) {
+// x = code * scale, the scale of a checkpoint's group (exps) or of the row
+// (scale), rounded once to T (exact for a checkpoint).
+template <typename T, int N>
+__global__ void __launch_bounds__(128) expand_kernel(const int8_t* __restrict__ codes,
+                                                     const uint8_t* __restrict__ exps,
+                                                     const float* __restrict__ scale, int64_t rows, int d,
+                                                     T* __restrict__ x) {
   const int lane = threadIdx.x & 31;
   const int ng = (d + GROUP - 1) / GROUP;
-  const int chunks = (d + 32 * V - 1) / (32 * V);
-  const int64_t items = T_ * chunks;
-  const int64_t nw = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
-  for (int64_t it = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); it < items; it += nw) {
-    const int64_t row = it / chunks;
-    const int c = static_cast<int>(it - row * chunks) * 32 * V + lane * V;
-    if (c >= d) continue;
-    const float s = exponent_value(exps[row * ng + c / GROUP]);
-    float v[V];
-    if constexpr (V == 1) {
-      v[0] = static_cast<float>(codes[row * d + c]) * s;
-    } else {
-      const uint2 w = *reinterpret_cast<const uint2*>(codes + row * d + c);
+  const int c0 = (blockIdx.x * 4 + (threadIdx.x >> 5)) * chunk_cols<N>;
+  if (c0 >= d) return;
+  for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
+    const int64_t at = row * d;
+    if constexpr (N == 1) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] = static_cast<float>(static_cast<int8_t>(w.x >> (8 * e))) * s;
-        v[4 + e] = static_cast<float>(static_cast<int8_t>(w.y >> (8 * e))) * s;
+      for (int g = 0; g < kOddGroups; ++g) {
+        const int c = c0 + g * GROUP + lane;
+        if (c < d) {
+          const float s = exps ? exponent_value(exps[row * ng + c / GROUP]) : scale[row];
+          x[at + c] = from_f32<T>(static_cast<float>(codes[at + c]) * s);
+        }
+      }
+    } else {
+      const int c = c0 + lane * N;
+      if (c < d) {
+        uint32_t w[N / 4];
+        load_codes<N>(codes + at + c, w);
+        const float s = exps ? exponent_value(exps[row * ng + c / GROUP]) : scale[row];
+        float v[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] = code_value(w, e) * s;
+        store_units<T, N>(x + at + c, v);
       }
     }
-    store_vec<T, V>(x + row * d + c, v);
   }
 }
 

@@ -50,38 +50,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T* __restrict_
   }
 }
 
-// w = code * scale (fp32 product), rounded once to the weight dtype.
-template <typename T>
-__global__ void dequantize_rows_kernel(const int8_t* __restrict__ Wq, const float* __restrict__ scale, int64_t rows,
-                                       int cols, T* __restrict__ W) {
-  const int64_t n = rows * cols;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const float v = static_cast<float>(Wq[i]) * scale[i / cols];
-    if constexpr (std::is_same<T, float>::value) W[i] = v;
-    else W[i] = __float2bfloat16_rn(v);
-  }
-}
-
-// 16 codes per thread (one 16-byte load, two 16-byte bf16 stores); cols % 16 == 0.
-__global__ void dequantize_rows_bf16x16_kernel(const int8_t* __restrict__ Wq, const float* __restrict__ scale,
-                                               int64_t rows, int cols, __nv_bfloat16* __restrict__ W) {
-  const int64_t n16 = rows * cols / 16;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n16;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const float s = scale[(i * 16) / cols];
-    const int4 codes = reinterpret_cast<const int4*>(Wq)[i];
-    const int8_t* c = reinterpret_cast<const int8_t*>(&codes);
-    uint4 out[2];
-    uint32_t* o = reinterpret_cast<uint32_t*>(out);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      __nv_bfloat162 h = __floats2bfloat162_rn(static_cast<float>(c[2 * k]) * s, static_cast<float>(c[2 * k + 1]) * s);
-      o[k] = *reinterpret_cast<uint32_t*>(&h);
-    }
-    reinterpret_cast<uint4*>(W)[2 * i] = out[0];
-    reinterpret_cast<uint4*>(W)[2 * i + 1] = out[1];
-  }
-}
+// (w = code * scale, rounded once to the weight dtype, is q8::expand_kernel in
+// q8.cuh, which reads any rows of codes.)
 
 }  // namespace poetx

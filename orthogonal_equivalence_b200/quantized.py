@@ -49,6 +49,12 @@ class Checkpoint(NamedTuple):
 
 def _like(t, name: str, dtype=None, shape=None, device=None) -> None:
     """Host-side check of a tensor before its pointer goes to the library."""
+    try:  # the good case, at the cost of a few attribute reads
+        if ((dtype is None or t.dtype == dtype) and (shape is None or t.shape == shape)
+                and (device is None or t.device == device) and t.is_contiguous()):
+            return
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if dtype is not None and t.dtype != dtype:
@@ -57,8 +63,7 @@ def _like(t, name: str, dtype=None, shape=None, device=None) -> None:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if device is not None and t.device != device:
         raise ValueError(f"{name}: tensor on {t.device}, the other operands are on {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
+    raise ValueError(f"{name}: must be contiguous")
 
 
 def _rows(t, name: str) -> Tuple[int, int]:
@@ -66,27 +71,38 @@ def _rows(t, name: str) -> Tuple[int, int]:
     _like(t, name)
     if t.dtype not in _DTYPE:
         raise ValueError(f"{name}: dtype {t.dtype}, expected torch.bfloat16 or torch.float32")
-    if t.dim() != 2 or t.shape[1] == 0:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [T][d] with d >= 1")
-    return t.shape[0], t.shape[1]
+    shape = t.shape
+    if len(shape) != 2 or shape[1] == 0:
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected [T][d] with d >= 1")
+    return shape
 
 
 def _codes(t, name: str) -> Tuple[int, int]:
     _like(t, name, torch.int8)
-    if t.dim() != 2 or t.shape[1] == 0:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [rows][d] with d >= 1")
-    return t.shape[0], t.shape[1]
+    shape = t.shape
+    if len(shape) != 2 or shape[1] == 0:
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected [rows][d] with d >= 1")
+    return shape
+
+
+_calls = {}
 
 
 def _run(device: torch.device, fn: str, *args) -> None:
     """The C call on the current stream of `device`, with that device current."""
     if device.type != "cuda":
         raise ValueError(f"tensors on {device}: the library runs on CUDA devices")
-    if device.index == torch.cuda.current_device():
-        _check(getattr(lib(), fn)(*args, torch.cuda.current_stream().cuda_stream), fn)
+    call = _calls.get(fn)
+    if call is None:
+        call = _calls[fn] = getattr(lib(), fn)
+    index = device.index
+    if index == torch.cuda.current_device():
+        status = call(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            _check(getattr(lib(), fn)(*args, torch.cuda.current_stream().cuda_stream), fn)
+            status = call(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        _check(status, fn)
 
 
 def _p(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -99,7 +115,7 @@ def quantize_rows(x: torch.Tensor, colscale: Optional[torch.Tensor] = None) -> Q
     dev = x.device
     if colscale is not None:
         _like(colscale, "colscale", torch.float32, (d,), dev)
-    out = QuantRows(torch.empty((T, d), dtype=torch.int8, device=dev),
+    out = QuantRows(torch.empty_like(x, dtype=torch.int8),
                     torch.empty(T, dtype=torch.float32, device=dev))
     _run(dev, "poetx_quantize_rows", T, d, x.data_ptr(), _DTYPE[x.dtype], _p(colscale), out.codes.data_ptr(),
          out.scale.data_ptr())
@@ -113,7 +129,7 @@ def dequantize_rows(codes: torch.Tensor, scale: torch.Tensor, dtype: torch.dtype
     _like(scale, "scale", torch.float32, (T,), dev)
     if dtype not in _DTYPE:
         raise ValueError(f"dtype: {dtype}, expected torch.bfloat16 or torch.float32")
-    out = torch.empty((T, d), dtype=dtype, device=dev)
+    out = torch.empty_like(codes, dtype=dtype)
     _run(dev, "poetx_weight_dequantize", T, d, codes.data_ptr(), scale.data_ptr(), _DTYPE[dtype], out.data_ptr())
     return out
 
@@ -129,7 +145,7 @@ def rmsnorm_quantize(x: torch.Tensor, gamma: torch.Tensor, residual: Optional[to
     if residual is not None:
         _like(residual, "residual", dt, x.shape, dev)
         h = torch.empty_like(x)
-    q = torch.empty((T, d), dtype=torch.int8, device=dev) if codes else None
+    q = torch.empty_like(x, dtype=torch.int8) if codes else None
     s = torch.empty(T, dtype=torch.float32, device=dev) if codes else None
     out = torch.empty_like(x) if y else None
     rstd = torch.empty(T, dtype=torch.float32, device=dev)
@@ -157,7 +173,7 @@ def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, gamma: torch.Tensor, rst
     else:
         dgamma = torch.empty(d, dtype=torch.float32, device=dev)
     dx = torch.empty_like(dy)
-    nb = poetx_rmsnorm_backward_workspace_bytes(T, d)
+    nb = poetx_rmsnorm_backward_workspace_bytes(T, d, _DTYPE[dt])
     ws = torch.empty(nb, dtype=torch.uint8, device=dev)
     _run(dev, "poetx_rmsnorm_backward", T, d, dy.data_ptr(), h.data_ptr(), gamma.data_ptr(), rstd.data_ptr(),
          _p(dres), _DTYPE[dt], dx.data_ptr(), dgamma.data_ptr(), int(accumulate), ws.data_ptr(), nb)
@@ -170,14 +186,17 @@ def matmul_int8(xq: torch.Tensor, xscale: torch.Tensor, Wq: torch.Tensor, wscale
     T, m = _codes(xq, "xq")
     dev = xq.device
     n, _ = _codes(Wq, "Wq")
-    _like(Wq, "Wq", torch.int8, (n, m), dev)
+    if Wq.shape[1] != m or Wq.device != dev:
+        _like(Wq, "Wq", torch.int8, (n, m), dev)
     _like(xscale, "xscale", torch.float32, (T,), dev)
     _like(wscale, "wscale", torch.float32, (n,), dev)
     if dtype not in _DTYPE:
         raise ValueError(f"dtype: {dtype}, expected torch.bfloat16 or torch.float32")
     out = torch.empty((T, n), dtype=dtype, device=dev)
-    nb = poetx_matmul_int8_workspace_bytes(T, n, m)
-    ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
+    nb, ws = 0, None
+    if m % 16:  # rows that are no whole 16-byte units are copied first
+        nb = poetx_matmul_int8_workspace_bytes(T, n, m)
+        ws = torch.empty(nb, dtype=torch.uint8, device=dev)
     _run(dev, "poetx_matmul_int8", T, n, m, xq.data_ptr(), xscale.data_ptr(), Wq.data_ptr(), wscale.data_ptr(),
          _DTYPE[dtype], out.data_ptr(), _p(ws), nb)
     return out
@@ -189,7 +208,8 @@ def matmul_int8_grad(dz: torch.Tensor, Wq: torch.Tensor, wscale: torch.Tensor) -
     T, n = _rows(dz, "dz")
     dev = dz.device
     _, m = _codes(Wq, "Wq")
-    _like(Wq, "Wq", torch.int8, (n, m), dev)
+    if Wq.shape[0] != n or Wq.device != dev:
+        _like(Wq, "Wq", torch.int8, (n, m), dev)
     _like(wscale, "wscale", torch.float32, (n,), dev)
     dx = torch.empty((T, m), dtype=dz.dtype, device=dev)
     nb = poetx_matmul_int8_grad_workspace_bytes(T, n, m)
@@ -203,7 +223,7 @@ def checkpoint_save(x: torch.Tensor) -> Checkpoint:
     """x as int8 codes with a shared power of two per 32 columns."""
     T, d = _rows(x, "x")
     dev = x.device
-    out = Checkpoint(torch.empty((T, d), dtype=torch.int8, device=dev),
+    out = Checkpoint(torch.empty_like(x, dtype=torch.int8),
                      torch.empty((T, (d + 31) // 32), dtype=torch.uint8, device=dev))
     _run(dev, "poetx_checkpoint_save", T, d, x.data_ptr(), _DTYPE[x.dtype], out.codes.data_ptr(),
          out.exps.data_ptr())
@@ -222,7 +242,7 @@ def checkpoint_load(ckpt: Checkpoint, dtype: torch.dtype) -> torch.Tensor:
     if dtype not in _DTYPE:
         raise ValueError(f"dtype: {dtype}, expected torch.bfloat16 or torch.float32")
     dev = ckpt.codes.device
-    out = torch.empty((T, d), dtype=dtype, device=dev)
+    out = torch.empty_like(ckpt.codes, dtype=dtype)
     _run(dev, "poetx_checkpoint_load", T, d, ckpt.codes.data_ptr(), ckpt.exps.data_ptr(), _DTYPE[dtype],
          out.data_ptr())
     return out

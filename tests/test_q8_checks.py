@@ -41,8 +41,8 @@ def test_statuses_of_the_norm(lib):
     assert n(4, 64, P, None, None, 1e-5, 1, None, None, P, P, P, None) == 1
     assert n(4, 64, P, None, P, 1e-5, 1, None, ODD, P, P, P, None) == 4
     b = lib.poetx_rmsnorm_backward
-    need = px.poetx_rmsnorm_backward_workspace_bytes(4, 64)
-    assert need > 0 and px.poetx_rmsnorm_backward_workspace_bytes(4, 51201) == 0
+    need = px.poetx_rmsnorm_backward_workspace_bytes(4, 64, 1)
+    assert need > 0 and px.poetx_rmsnorm_backward_workspace_bytes(4, 51201, 1) == 0
     assert b(4, 64, P, P, P, P, None, 1, P, P, 0, P, need - 1, None) == 5
     assert b(4, 64, P, P, P, P, None, 1, P, P, 0, None, need, None) == 5
     assert b(4, 64, P, P, P, None, None, 1, P, P, 0, P, need, None) == 1
