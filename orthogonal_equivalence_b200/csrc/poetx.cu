@@ -23,6 +23,7 @@
 #include "cnp2build.cuh"
 #include "bdg2sm.cuh"
 #include "q8.cuh"
+#include "bdg8.cuh"
 #include "gemm_i8.cuh"
 
 using namespace poetx;
@@ -2139,9 +2140,90 @@ size_t grad_i8_ws(int64_t T, int32_t n, int32_t m) {
   return kAlign + al(size_t(T) * row16(n)) + al(sizeof(float) * size_t(T)) + (m % 16 ? al(size_t(n) * row16(m)) : 0);
 }
 
+// ---- backward of one side from a checkpoint (bdg8.cuh for b = 256 bf16)
+bool use_pair_bdg8(int32_t b, int32_t dtype) { return b == bdg2::BLK && dtype == POETX_BF16; }
+
+// Token splits: about SPLIT_TOKENS each at most, and of the counts up to half
+// as many again the one that leaves the fewest pairs of SMs idle in the last
+// round (16 blocks in 8 splits keep 128 of 2 x 74 pairs busy, in 9 splits 144).
+int bdg8_splits(int nblk, int64_t T) {
+  constexpr int pairs = kSplitSMs / 2;
+  const int64_t ntiles = (T + bdg2::BLK - 1) / bdg2::BLK;
+  int64_t lo = (T + bdg8::SPLIT_TOKENS - 1) / bdg8::SPLIT_TOKENS;
+  const int64_t fill = (pairs + nblk - 1) / nblk;   // one round of the pairs, if the tokens allow four tiles a split
+  if (lo < fill) lo = fill < ntiles / 4 ? fill : ntiles / 4 > lo ? ntiles / 4 : lo;
+  if (lo < 1) lo = 1;
+  int best = static_cast<int>(lo);
+  double best_use = 0.0;
+  for (int64_t s = lo; s <= lo + lo / 2 && s <= ntiles; ++s) {
+    const int64_t items = nblk * s, rounds = (items + pairs - 1) / pairs;
+    const double use = static_cast<double>(items) / (rounds * pairs);
+    if (use > best_use + 0.02) {
+      best_use = use;
+      best = static_cast<int>(s);
+    }
+  }
+  return best;
+}
+
+int block_backward_splits(int64_t T, int32_t d, int32_t b, int32_t dtype) {
+  return use_pair_bdg8(b, dtype) ? bdg8_splits(d / b, T) : dg_splits(d / b, b, T, dtype);
+}
+
+cudaError_t launch_bdg8(const void* D, const int8_t* codes, const uint8_t* exps, const void* G, void* O, float* part,
+                        int64_t T, int d, int splits, cudaStream_t st, int device) {
+  static bool attr_set[64] = {false};
+  if (device >= 0 && device < 64 && !attr_set[device]) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(bdg8::bdg8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bdg8::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    attr_set[device] = true;
+  }
+  const int nblk = d / bdg2::BLK;
+  auto view = [](const void* ptr, int64_t rows, int64_t cols) {
+    Operand2D v;
+    v.ptr = ptr;
+    v.et = ET_BF16;
+    v.rows = rows;
+    v.cols = cols;
+    v.ld = cols;
+    return v;
+  };
+  CUtensorMap mDk, mDmn, mX, mG, mO, mPart;
+  Operand2D pv = view(part, int64_t(splits) * nblk * bdg2::BLK, bdg2::BLK);
+  pv.et = ET_F32;
+  if (!encode_map(&mDk, view(D, T, d), bdg2::HALF) || !encode_map(&mDmn, view(D, T, d), bdg2::CH) ||
+      !encode_bytes_map(&mX, codes, T, d, d, bdg2::CH) || !encode_map(&mPart, pv, 32))
+    return cudaErrorInvalidValue;
+  mG = mO = mDk;  // unused without O
+  if (O && (!encode_map(&mG, view(G, int64_t(nblk) * bdg2::BLK, bdg2::BLK), bdg2::HALF) ||
+            !encode_map(&mO, view(O, T, d), 32)))
+    return cudaErrorInvalidValue;
+  bdg8::Params p;
+  p.g.T = static_cast<int>(T);
+  p.g.nblk = nblk;
+  p.g.splits = splits;
+  p.g.ntiles = static_cast<int>((T + bdg2::BLK - 1) / bdg2::BLK);
+  p.g.want_o = O ? 1 : 0;
+  // D fp32, A and B bf16, N = 256 (bits 17-22: N >> 3), M = 256 (bits 24-28: M >> 4);
+  // bit 15: A MN-major, bit 16: B MN-major
+  p.g.idesc_kk = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(bdg2::BLK >> 3) << 17) |
+                 (static_cast<uint32_t>(bdg2::BLK >> 4) << 24);
+  p.g.idesc_mnmn = p.g.idesc_kk | (1u << 15) | (1u << 16);
+  p.g.part = part;
+  p.exps = exps;
+  p.ng = d / q8::GROUP;
+  const int items = nblk * splits;
+  const int pairs = sm_count(device) / 2 < items ? sm_count(device) / 2 : items;
+  bdg8::bdg8_pair_kernel<<<2 * pairs, bdg8::NUM_THREADS, bdg8::SMEM_BYTES, st>>>(mDk, mDmn, mX, mG, mO,
+                                                                                      mPart, p);
+  return cudaGetLastError();
+}
+
+// Workspace: the partial sums, and X expanded where no kernel reads the codes.
 size_t block_backward_ws(int64_t T, int32_t d, int32_t b, int32_t dtype) {
-  return kAlign + al(size_t(dtype_size(dtype)) * T * d) +
-         al(sizeof(float) * size_t(dg_splits(d / b, b, T, dtype)) * d * b);
+  return kAlign + (use_pair_bdg8(b, dtype) ? 0 : al(size_t(dtype_size(dtype)) * T * d)) +
+         al(sizeof(float) * size_t(block_backward_splits(T, d, b, dtype)) * d * b);
 }
 
 poetx_status check_block(int64_t T, int32_t d, int32_t b, int32_t dtype) {
@@ -2363,18 +2445,18 @@ poetx_status poetx_block_backward(int64_t T, int32_t d, int32_t b, const int8_t*
   if (!ws || ws_bytes < block_backward_ws(T, d, b, dtype)) return POETX_E_WORKSPACE;
   int dev;
   POETX_TRY(current_device(&dev));
-  const int et = elem_type(dtype), nb = d / b;
+  const int et = elem_type(dtype);
   const bool tc_path = use_tc(dtype);
-  const int splits = dg_splits(nb, b, T, dtype);
+  const int splits = block_backward_splits(T, d, b, dtype);
   const size_t elems = size_t(d) * b;
   Carver c(ws, ws_bytes);
-  void* X = c.take<uint8_t>(size_t(dtype_size(dtype)) * T * d);
   float* part = c.take<float>(sizeof(float) * splits * elems);
-  POETX_CUDA(checkpoint_load(T, d, codes, exps, dtype, X, st, dev));
   if (splits == 1 && !accumulate) part = dG;
-  if (dtype == POETX_BF16 && b == bdg2::BLK) {
-    PROFILED(ST_BDG, st, POETX_CUDA(launch_bdg(D, X, O ? G : D, O, part, T, d, splits, st, dev)));
+  if (use_pair_bdg8(b, dtype)) {
+    PROFILED(ST_BDG, st, POETX_CUDA(launch_bdg8(D, codes, exps, G, O, part, T, d, splits, st, dev)));
   } else {
+    void* X = c.take<uint8_t>(size_t(dtype_size(dtype)) * T * d);
+    POETX_CUDA(checkpoint_load(T, d, codes, exps, dtype, X, st, dev));
     if (O) PROFILED(ST_BLOCKDIAG, st, POETX_CUDA(launch_gemm(blockdiag_desc(D, et, T, d, b, G, true, O, et), tc_path, st, dev)));
     PROFILED(ST_DG, st, POETX_CUDA(launch_gemm(blockgrad_desc(X, D, et, T, d, b, splits, part), tc_path, st, dev)));
   }

@@ -350,7 +350,7 @@ def test_checkpoint_nonfinite_groups(d):
 
 
 BLOCK = [(BF, 1, 64, 64), (BF, 77, 192, 64), (BF, 300, 512, 128), (BF, 257, 1024, 256), (BF, 1, 256, 256),
-         (BF, 1000, 768, 256), (BF, 2100, 256, 256), (BF, 130, 1024, 512), (F32, 1, 2, 2), (F32, 65, 9, 3),
+         (BF, 1000, 768, 256), (BF, 2100, 256, 256), (BF, 5000, 2304, 256), (BF, 9001, 512, 256), (BF, 130, 1024, 512), (F32, 1, 2, 2), (F32, 65, 9, 3),
          (F32, 300, 512, 64), (F32, 1001, 80, 40), (F32, 40, 100, 100)]
 
 
