@@ -72,18 +72,42 @@ __device__ __forceinline__ void arrive_pair(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-// Eight codes (two words) times s as bf16, packed.
+// Eight codes (two words) times s as bf16, packed.  A byte code + 128 under the
+// exponent of 2^23 is the fp32 number 2^23 + 128 + code; one FMA with s and
+// (2^23 + 128) s gives code * s without a rounding (two at a time), as long as
+// (2^23 + 128) s is finite: FAR takes the others, 2^100 and up.
+__device__ __forceinline__ uint32_t fma_pair(float x, float y, uint64_t s2, uint64_t c2) {
+  uint32_t r;
+  asm("{\n\t.reg .b64 v;\n\t.reg .f32 a, b;\n\t"
+      "mov.b64 v, {%1, %2};\n\t"
+      "fma.rn.f32x2 v, v, %3, %4;\n\t"
+      "mov.b64 {a, b}, v;\n\t"
+      "cvt.rn.bf16x2.f32 %0, b, a;\n\t}"
+      : "=r"(r)
+      : "f"(x), "f"(y), "l"(s2), "l"(c2));
+  return r;
+}
+__device__ __forceinline__ uint64_t twice(float f) {
+  const uint64_t b = __float_as_uint(f);
+  return b << 32 | b;
+}
+template <bool FAR>
 __device__ __forceinline__ uint4 expand8(uint32_t w0, uint32_t w1, float s) {
   uint32_t o[4];
+  const uint64_t s2 = twice(s), c2 = twice(-8388736.f * s);
   const uint32_t b[2] = {w0 ^ 0x80808080u, w1 ^ 0x80808080u};  // code + 128
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     float f[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)  // 2^23 + code + 128, exactly
-      f[e] = (__uint_as_float(__byte_perm(b[i], 0x4b000000u, 0x7540 + e)) - 8388736.f) * s;
-    o[2 * i] = pack_bf16x2(f[0], f[1]);
-    o[2 * i + 1] = pack_bf16x2(f[2], f[3]);
+    for (int e = 0; e < 4; ++e) f[e] = __uint_as_float(__byte_perm(b[i], 0x4b000000u, 0x7540 + e));
+    if (FAR) {
+      o[2 * i] = pack_bf16x2((f[0] - 8388736.f) * s, (f[1] - 8388736.f) * s);
+      o[2 * i + 1] = pack_bf16x2((f[2] - 8388736.f) * s, (f[3] - 8388736.f) * s);
+    } else {
+      o[2 * i] = fma_pair(f[0], f[1], s2, c2);
+      o[2 * i + 1] = fma_pair(f[2], f[3], s2, c2);
+    }
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
@@ -301,12 +325,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     // tile ahead (rows behind the last token: 0, which reads as 0 like their
     // codes).
     uint32_t ex[4];
-    auto exponents = [&](int item, int tile, int c) {
-      const int64_t token = int64_t(tile) * BLK + c * CH + row;
-      const int group = ((item % p.nblk) * BLK + int(rank) * HALF + half * CH) / q8::GROUP;
-      ex[c] = 0;
-      if (item < items && token < p.T)
-        ex[c] = __ldg(reinterpret_cast<const unsigned short*>(pp.exps + token * pp.ng + group));
+    auto exponents_of = [&](int item) {  // of the item's block, first row of this thread
+      return pp.exps + ((item % p.nblk) * BLK + int(rank) * HALF + half * CH) / q8::GROUP + int64_t(row) * pp.ng;
+    };
+    auto exponents = [&](const uint8_t* of, int token0, int c) {
+      ex[c] = token0 + c * CH + row < p.T
+                  ? __ldg(reinterpret_cast<const unsigned short*>(of + int64_t(token0 + c * CH) * pp.ng))
+                  : 0;
     };
     int u = 0, slot = 0;
     uint32_t ring = 0, cring = 0;
@@ -315,16 +340,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     if (pair < items) {
       bdg2::split_tiles(p, pair / p.nblk, ta, tb);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) exponents(pair, ta, c);
+      for (int c = 0; c < 4; ++c) exponents(exponents_of(pair), ta * BLK, c);
     }
     for (int item = pair; item < items && ok; item += npairs) {
       bdg2::split_tiles(p, item / p.nblk, ta, tb);
+      const uint8_t* of = exponents_of(item);
       for (int tile = ta; tile < tb && ok; ++tile) {
-        int nitem = item, ntile = tile + 1;  // the tile after this one
-        if (ntile == tb) {
-          nitem = item + npairs;
-          int last;
-          bdg2::split_tiles(p, nitem / p.nblk, ntile, last);
+        int next0 = (tile + 1) * BLK;  // first token of the tile after this one
+        if (tile + 1 == tb) {
+          int first, last;
+          bdg2::split_tiles(p, (item + npairs) / p.nblk, first, last);
+          next0 = item + npairs < items ? first * BLK : p.T;
+          of = exponents_of(item + npairs);
         }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -333,7 +360,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           ok = __all_sync(0xffffffffu, ok);
           if (ok) {
             const float s0 = q8::exponent_value(ex[c] & 0xffu), s1 = q8::exponent_value(ex[c] >> 8);
-            exponents(nitem, ntile, c);
+            exponents(of, next0, c);
             const uint32_t src = sCode + slot * SLOT_BYTES + row * 128;
             const uint32_t dst = sX + u * TILE_BYTES + half * (CH * 128) + row * 128;
             uint32_t w[4][4];
@@ -343,15 +370,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                            : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
                            : "r"(src + (((half * 4 + i) ^ (row & 7)) << 4))
                            : "memory");
+            auto put = [&](auto far) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+              for (int i = 0; i < 4; ++i)
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint4 o = expand8(w[i][2 * h], w[i][2 * h + 1], i < 2 ? s0 : s1);
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (((2 * i + h) ^ (row & 7)) << 4)),
-                             "r"(o.x), "r"(o.y), "r"(o.z), "r"(o.w)
-                             : "memory");
-              }
+                for (int h = 0; h < 2; ++h) {
+                  const uint4 o = expand8<decltype(far)::value>(w[i][2 * h], w[i][2 * h + 1], i < 2 ? s0 : s1);
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (((2 * i + h) ^ (row & 7)) << 4)),
+                               "r"(o.x), "r"(o.y), "r"(o.z), "r"(o.w)
+                               : "memory");
+                }
+            };
+            if (s0 >= 0x1p100f || s1 >= 0x1p100f) put(std::true_type());
+            else put(std::false_type());
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {

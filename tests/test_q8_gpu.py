@@ -376,6 +376,20 @@ def test_block_backward(dtype, T, d, b):
     within(acc, 2 + dG.double(), 2 * U24 * (2 + dG.double().abs()), "accumulated dG")
 
 
+@pytest.mark.parametrize("power", [-110, -60, 90, 112, 119])
+def test_block_backward_over_the_range_of_exponents(power):
+    # checkpoints near both ends of the exponents' range, D scaled the other way: the products stay ordinary
+    T, d, b = 300, 256, 256
+    x = rnd(60, T, d) * 2.0 ** power
+    D = (rnd(61, T, d) * 2.0 ** max(-110, -power)).to(BF)
+    c = px.checkpoint_save(x)
+    _, dG = px.block_backward(c, D, torch.zeros(1, b, b, dtype=BF, device="cuda"))
+    X = px.checkpoint_load(c, F32).double()
+    assert torch.isfinite(X).all()
+    tol = 2 * (T + 34) * U24 * (X.abs().t() @ D.double().abs())
+    within(dG[0], X.t() @ D.double(), tol, "dG")
+
+
 def test_block_backward_nan_group_reaches_its_gradient():
     T, d, b = 40, 512, 256
     x, D, G = rnd(42, T, d, dtype=BF), rnd(43, T, d, dtype=BF), rnd(44, 2, b, b, dtype=BF)
