@@ -24,6 +24,7 @@
 #include "bdg2sm.cuh"
 #include "q8.cuh"
 #include "bdg8.cuh"
+#include "block_f32.cuh"
 #include "gemm_i8.cuh"
 
 using namespace poetx;
@@ -2166,8 +2167,45 @@ int bdg8_splits(int nblk, int64_t T) {
   return best;
 }
 
+// fp32: tiles of 32 where 64 would stand half empty; the tokens split until
+// six blocks a SM have work, with 64 tokens a split at least.
+int block_f32_tile(int b) { return b <= 32 ? 32 : 64; }
+int block_f32_splits(int nblk, int b, int64_t T) {
+  const int64_t tb = (b + block_f32_tile(b) - 1) / block_f32_tile(b);
+  int64_t s = 6 * kSplitSMs / (nblk * tb * tb);
+  if (s > T / 64) s = T / 64;
+  return s < 1 ? 1 : s > 32 ? 32 : static_cast<int>(s);
+}
+
 int block_backward_splits(int64_t T, int32_t d, int32_t b, int32_t dtype) {
+  if (dtype == POETX_FP32) return block_f32_splits(d / b, b, T);
   return use_pair_bdg8(b, dtype) ? bdg8_splits(d / b, T) : dg_splits(d / b, b, T, dtype);
+}
+
+cudaError_t launch_block_f32(const void* D, const int8_t* codes, const uint8_t* exps, const void* G, void* O,
+                             float* part, int64_t T, int d, int b, int splits, cudaStream_t st) {
+  const int ts = block_f32_tile(b);
+  bf32::Params p;
+  p.D = static_cast<const float*>(D);
+  p.G = static_cast<const float*>(G);
+  p.O = static_cast<float*>(O);
+  p.codes = codes;
+  p.exps = exps;
+  p.part = part;
+  p.T = T;
+  p.d = d;
+  p.b = b;
+  p.ng = (d + q8::GROUP - 1) / q8::GROUP;
+  p.nblk = d / b;
+  p.splits = splits;
+  p.tiles_b = (b + ts - 1) / ts;
+  p.o_blocks = O ? (T + ts - 1) / ts * p.nblk * p.tiles_b : 0;
+  const int64_t blocks = p.o_blocks + int64_t(splits) * p.nblk * p.tiles_b * p.tiles_b;
+  if (blocks > 2147483647) return cudaErrorInvalidValue;
+  const unsigned grid = static_cast<unsigned>(blocks);
+  if (ts == 32) bf32::block_backward_kernel<32><<<grid, bf32::THREADS, 0, st>>>(p);
+  else bf32::block_backward_kernel<64><<<grid, bf32::THREADS, 0, st>>>(p);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_bdg8(const void* D, const int8_t* codes, const uint8_t* exps, const void* G, void* O, float* part,
@@ -2222,7 +2260,7 @@ cudaError_t launch_bdg8(const void* D, const int8_t* codes, const uint8_t* exps,
 
 // Workspace: the partial sums, and X expanded where no kernel reads the codes.
 size_t block_backward_ws(int64_t T, int32_t d, int32_t b, int32_t dtype) {
-  return kAlign + (use_pair_bdg8(b, dtype) ? 0 : al(size_t(dtype_size(dtype)) * T * d)) +
+  return kAlign + (use_pair_bdg8(b, dtype) || dtype == POETX_FP32 ? 0 : al(size_t(dtype_size(dtype)) * T * d)) +
          al(sizeof(float) * size_t(block_backward_splits(T, d, b, dtype)) * d * b);
 }
 
@@ -2454,6 +2492,8 @@ poetx_status poetx_block_backward(int64_t T, int32_t d, int32_t b, const int8_t*
   if (splits == 1 && !accumulate) part = dG;
   if (use_pair_bdg8(b, dtype)) {
     PROFILED(ST_BDG, st, POETX_CUDA(launch_bdg8(D, codes, exps, G, O, part, T, d, splits, st, dev)));
+  } else if (dtype == POETX_FP32) {
+    PROFILED(ST_BDG, st, POETX_CUDA(launch_block_f32(D, codes, exps, G, O, part, T, d, b, splits, st)));
   } else {
     void* X = c.take<uint8_t>(size_t(dtype_size(dtype)) * T * d);
     POETX_CUDA(checkpoint_load(T, d, codes, exps, dtype, X, st, dev));
