@@ -353,6 +353,37 @@ poetx_status poetx_block_backward(int64_t T, int32_t d, int32_t b, const int8_t*
                                   const void* D, const void* G, int32_t dtype, void* O, float* dG,
                                   int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
 
+/* The layer in 8 bits: poetx_forward, poetx_backward and poetx_backward_dG
+ * with, each where its pointers are set (device memory, 16-byte aligned),
+ *   Wq, wscale: the stored weight as poetx_weight_quantize wrote it.  The W0
+ *     product then runs in int8: Y = rows(U) Wq^T as in poetx_matmul_int8 with
+ *     U = Xg Diag(G_R) quantised row by row, and dU as in
+ *     poetx_matmul_int8_grad.  layer->W is not read (it must not be NULL).
+ *   y_codes, y_exps / xg_codes, xg_exps: checkpoints (poetx_checkpoint_save)
+ *     of Y [T][n] and Xg [T][m], written by the forward and read by the
+ *     backward in the place of y_save / xg_save, which must be NULL then.  z
+ *     and dx are those of the calls without; the dG sums see the checkpoints'
+ *     values.  A backward without Y in either form recomputes it from Xg.
+ * layer->fold must be 0 (POETX_E_ARG).  have_y: y_save will be given. */
+typedef struct {
+  const int8_t* Wq;     /* [n][m] or NULL */
+  const float* wscale;  /* [n] */
+  int8_t* y_codes;      /* [T][n] or NULL */
+  uint8_t* y_exps;      /* [T][ceil(n / 32)] */
+  int8_t* xg_codes;     /* [T][m] or NULL */
+  uint8_t* xg_exps;     /* [T][ceil(m / 32)] */
+} poetx_q8;
+size_t poetx_forward_q8_workspace_bytes(const poetx_layer* layer, int64_t T, const poetx_q8* q8);
+poetx_status poetx_forward_q8(const poetx_layer* layer, int64_t T, const void* x, void* z, void* y_save,
+                              void* xg_save, const poetx_q8* q8, void* ws, size_t ws_bytes, void* stream);
+size_t poetx_backward_q8_workspace_bytes(const poetx_layer* layer, int64_t T, int32_t have_y, const poetx_q8* q8);
+poetx_status poetx_backward_q8(const poetx_layer* layer, int64_t T, const void* x, const void* y_save,
+                               const void* xg_save, const poetx_q8* q8, const void* dz, void* dx, float* dqR,
+                               float* dqP, int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
+poetx_status poetx_backward_dG_q8(const poetx_layer* layer, int64_t T, const void* x, const void* y_save,
+                                  const void* xg_save, const poetx_q8* q8, const void* dz, void* dx, float* dGR,
+                                  float* dGP, int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
+
 /* Optimizer step on packed triangles (fp32, n entries): AdamW with decoupled
  * weight decay (the write-up names get_poet_optimizer without describing it;
  * AdamW is the reading taken): m1 <- b1 m1 + (1-b1) g; m2 <- b2 m2 + (1-b2) g^2;

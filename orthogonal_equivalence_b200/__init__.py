@@ -44,8 +44,14 @@ class poetx_layer(ctypes.Structure):
                 ("fold", ctypes.c_int32)]
 
 
+class poetx_q8(ctypes.Structure):
+    _fields_ = [("Wq", ctypes.c_void_p), ("wscale", ctypes.c_void_p), ("y_codes", ctypes.c_void_p),
+                ("y_exps", ctypes.c_void_p), ("xg_codes", ctypes.c_void_p), ("xg_exps", ctypes.c_void_p)]
+
+
 _VP, _I32, _I64, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _LP = ctypes.POINTER(poetx_layer)
+_QP = ctypes.POINTER(poetx_q8)
 
 # name -> (restype, argtypes); mirrors include/poetx.h
 SIGNATURES = {
@@ -89,6 +95,11 @@ SIGNATURES = {
     "poetx_block_backward_workspace_bytes": (_SZ, [_I64, _I32, _I32, _I32]),
     "poetx_block_backward": (ctypes.c_int, [_I64, _I32, _I32, _VP, _VP, _VP, _VP, _I32, _VP, _VP, _I32, _VP, _SZ,
                                             _VP]),
+    "poetx_forward_q8_workspace_bytes": (_SZ, [_LP, _I64, _QP]),
+    "poetx_forward_q8": (ctypes.c_int, [_LP, _I64, _VP, _VP, _VP, _VP, _QP, _VP, _SZ, _VP]),
+    "poetx_backward_q8_workspace_bytes": (_SZ, [_LP, _I64, _I32, _QP]),
+    "poetx_backward_q8": (ctypes.c_int, [_LP, _I64, _VP, _VP, _VP, _QP, _VP, _VP, _VP, _VP, _I32, _VP, _SZ, _VP]),
+    "poetx_backward_dG_q8": (ctypes.c_int, [_LP, _I64, _VP, _VP, _VP, _QP, _VP, _VP, _VP, _VP, _I32, _VP, _SZ, _VP]),
     "poetx_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_uint32, _VP, _VP]),
     "poetx_adamw_step": (ctypes.c_int, [_I64, _VP, _VP, _VP, _VP, ctypes.c_float, ctypes.c_float, ctypes.c_float,
                                         ctypes.c_float, ctypes.c_float, _I32, _VP]),
@@ -333,6 +344,38 @@ def poetx_block_backward(T: int, d: int, b: int, codes, exps, D, G, dtype: int, 
                                       accumulate, _ptr(ws), ws_bytes, _stream(stream)), "poetx_block_backward")
 
 
+def make_q8(Wq=None, wscale=None, y_codes=None, y_exps=None, xg_codes=None, xg_exps=None) -> poetx_q8:
+    return poetx_q8(_ptr(Wq), _ptr(wscale), _ptr(y_codes), _ptr(y_exps), _ptr(xg_codes), _ptr(xg_exps))
+
+
+def poetx_forward_q8_workspace_bytes(layer: poetx_layer, T: int, q8: poetx_q8) -> int:
+    return lib().poetx_forward_q8_workspace_bytes(ctypes.byref(layer), T, ctypes.byref(q8))
+
+
+def poetx_forward_q8(layer: poetx_layer, T: int, x, z, y_save, xg_save, q8: poetx_q8, ws, ws_bytes: int,
+                     stream=None) -> None:
+    _check(lib().poetx_forward_q8(ctypes.byref(layer), T, _ptr(x), _ptr(z), _ptr(y_save), _ptr(xg_save),
+                                  ctypes.byref(q8), _ptr(ws), ws_bytes, _stream(stream)), "poetx_forward_q8")
+
+
+def poetx_backward_q8_workspace_bytes(layer: poetx_layer, T: int, have_y: int, q8: poetx_q8) -> int:
+    return lib().poetx_backward_q8_workspace_bytes(ctypes.byref(layer), T, have_y, ctypes.byref(q8))
+
+
+def poetx_backward_q8(layer: poetx_layer, T: int, x, y_save, xg_save, q8: poetx_q8, dz, dx, dqR, dqP,
+                      accumulate: int, ws, ws_bytes: int, stream=None) -> None:
+    _check(lib().poetx_backward_q8(ctypes.byref(layer), T, _ptr(x), _ptr(y_save), _ptr(xg_save), ctypes.byref(q8),
+                                   _ptr(dz), _ptr(dx), _ptr(dqR), _ptr(dqP), accumulate, _ptr(ws), ws_bytes,
+                                   _stream(stream)), "poetx_backward_q8")
+
+
+def poetx_backward_dG_q8(layer: poetx_layer, T: int, x, y_save, xg_save, q8: poetx_q8, dz, dx, dGR, dGP,
+                         accumulate: int, ws, ws_bytes: int, stream=None) -> None:
+    _check(lib().poetx_backward_dG_q8(ctypes.byref(layer), T, _ptr(x), _ptr(y_save), _ptr(xg_save),
+                                      ctypes.byref(q8), _ptr(dz), _ptr(dx), _ptr(dGR), _ptr(dGP), accumulate,
+                                      _ptr(ws), ws_bytes, _stream(stream)), "poetx_backward_dG_q8")
+
+
 def poetx_adamw_step(n: int, q, grad, m1, m2, lr: float, beta1: float, beta2: float, eps: float,
                      weight_decay: float, step: int, stream=None) -> None:
     _check(lib().poetx_adamw_step(n, _ptr(q), _ptr(grad), _ptr(m1), _ptr(m2), lr, beta1, beta2, eps, weight_decay,
@@ -369,7 +412,7 @@ def poetx_profile_records() -> list:
     return [(names[st[i]], ms[i]) for i in range(n)]
 
 
-from .layer import LayerGroup, PoetxLinear, Saved  # noqa: E402,F401
 from .quantized import (Checkpoint, NormRows, QuantRows, block_backward, checkpoint_load, checkpoint_save,  # noqa: E402,F401
                         dequantize_rows, matmul_int8, matmul_int8_grad, quantize_rows, rmsnorm_backward,
                         rmsnorm_quantize)
+from .layer import Int8Linear, LayerGroup, PoetxLinear, Saved  # noqa: E402,F401

@@ -1014,698 +1014,9 @@ poetx_status cnp_backward2(int32_t b, int32_t dtype, const float* q0, int n0, co
 
 }  // namespace
 
-// ======================================================================== ABI
-
-extern "C" {
-
-const char* poetx_status_string(int status) {
-  switch (status) {
-    case POETX_OK: return "POETX_OK";
-    case POETX_E_ARG: return "POETX_E_ARG: null pointer, negative size or bad flag";
-    case POETX_E_SHAPE: return "POETX_E_SHAPE: b must divide m and n (and be a multiple of 64 for bf16)";
-    case POETX_E_DTYPE: return "POETX_E_DTYPE: unknown dtype";
-    case POETX_E_ALIGN: return "POETX_E_ALIGN: pointer not 16-byte aligned";
-    case POETX_E_WORKSPACE: return "POETX_E_WORKSPACE: workspace missing or too small";
-    case POETX_E_ARCH: return "POETX_E_ARCH: current device is not compute capability 10.0 (B200)";
-    case POETX_E_CUDA: return "POETX_E_CUDA: CUDA runtime error while queueing work";
-    default: return "POETX: unknown status";
-  }
-}
-
-int32_t poetx_version(void) { return 10100; }
-
-poetx_status poetx_device_error(uint32_t* code) {
-  if (!code) return POETX_E_ARG;
-  int dev;
-  POETX_TRY(current_device(&dev));
-  unsigned int v = 0, zero = 0;
-  POETX_CUDA(cudaDeviceSynchronize());
-  POETX_CUDA(cudaMemcpyFromSymbol(&v, g_device_error, sizeof(v)));
-  POETX_CUDA(cudaMemcpyToSymbol(g_device_error, &zero, sizeof(zero)));
-  *code = v;
-  return POETX_OK;
-}
-
-size_t poetx_cnp_workspace_bytes(int32_t nblk, int32_t b, int32_t dtype) {
-  (void)dtype;
-  if (nblk <= 0 || b < 2) return 0;
-  return kAlign + cnp_bwd_ws(nblk, b);
-}
-
-size_t poetx_layers_cnp_workspace_bytes(int32_t nlayers, const poetx_layer* layers) {
-  if (nlayers < 1 || 2 * nlayers > kMaxSegs || !layers) return 0;
-  int64_t nblk = 0;
-  for (int i = 0; i < nlayers; ++i) {
-    if (check_layer(&layers[i]) != POETX_OK || layers[i].b != layers[0].b || layers[i].dtype != layers[0].dtype)
-      return 0;
-    nblk += layers[i].m / layers[i].b + layers[i].n / layers[i].b;
-  }
-  const int b = layers[0].b;
-  return kAlign + 3 * cnp_units(static_cast<int32_t>(nblk), b) +
-         al(size_t(dtype_size(layers[0].dtype)) * size_t(nblk) * b * b);
-}
-
-poetx_status poetx_layers_cnp_build(int32_t nlayers, const poetx_layer* layers, void* ws, size_t ws_bytes,
-                                    void* stream) {
-  if (nlayers < 1 || 2 * nlayers > kMaxSegs || !layers) return POETX_E_ARG;
-  for (int i = 0; i < nlayers; ++i) {
-    POETX_TRY(check_layer(&layers[i]));
-    if (layers[i].b != layers[0].b) return POETX_E_SHAPE;
-    if (layers[i].dtype != layers[0].dtype) return POETX_E_DTYPE;
-  }
-  if (!ws || ws_bytes < poetx_layers_cnp_workspace_bytes(nlayers, layers)) return POETX_E_WORKSPACE;
-  int dev;
-  POETX_TRY(current_device(&dev));
-  Segs sg{};
-  sg.n = 2 * nlayers;
-  int blk = 0;
-  for (int i = 0; i < nlayers; ++i) {
-    const poetx_layer& L = layers[i];
-    sg.start[2 * i] = blk;
-    sg.q[2 * i] = L.qR;
-    sg.G[2 * i] = L.GR;
-    blk += L.m / L.b;
-    sg.start[2 * i + 1] = blk;
-    sg.q[2 * i + 1] = L.qP;
-    sg.G[2 * i + 1] = L.GP;
-    blk += L.n / L.b;
-  }
-  sg.start[sg.n] = blk;
-  Carver c(ws, ws_bytes);
-  return cnp_build_segs(layers[0].b, layers[0].dtype, sg, c, static_cast<cudaStream_t>(stream), dev);
-}
-
-size_t poetx_layer_cnp_workspace_bytes(const poetx_layer* layer) {
-  if (check_layer(layer) != POETX_OK) return 0;
-  return kAlign + cnp_bwd_ws(layer->m / layer->b + layer->n / layer->b, layer->b);
-}
-
-poetx_status poetx_layer_cnp_build(const poetx_layer* layer, void* ws, size_t ws_bytes, void* stream) {
-  POETX_TRY(check_layer(layer));
-  if (!ws || ws_bytes < poetx_layer_cnp_workspace_bytes(layer)) return POETX_E_WORKSPACE;
-  int dev;
-  POETX_TRY(current_device(&dev));
-  const poetx_layer& L = *layer;
-  Carver c(ws, ws_bytes);
-  return cnp_build2(L.b, L.dtype, L.qR, L.m / L.b, L.GR, L.qP, L.n / L.b, L.GP, c, static_cast<cudaStream_t>(stream),
-                    dev);
-}
-
-size_t poetx_forward_workspace_bytes(const poetx_layer* layer, int64_t T) {
-  if (check_layer(layer) != POETX_OK || T < 0 || T > kMaxT) return 0;
-  return fwd_ws(layer, T);
-}
-
-size_t poetx_backward_workspace_bytes(const poetx_layer* layer, int64_t T) {
-  if (check_layer(layer) != POETX_OK || T < 0 || T > kMaxT) return 0;
-  return bwd_ws(layer, T);
-}
-
-size_t poetx_backward_recompute_workspace_bytes(const poetx_layer* layer, int64_t T) {
-  if (check_layer(layer) != POETX_OK || T < 0 || T > kMaxT) return 0;
-  return bwd_recompute_ws(layer, T);
-}
-
-size_t poetx_merge_workspace_bytes(const poetx_layer* layer) {
-  if (check_layer(layer) != POETX_OK) return 0;
-  return merge_ws(layer);
-}
-
-size_t poetx_check_perm_workspace_bytes(int32_t len) {
-  if (len <= 0) return 0;
-  return kAlign + al(sizeof(int32_t) * size_t(len));
-}
-
-poetx_status poetx_frame_import(const poetx_layer* layer, const void* W0lin, void* stream) {
-  POETX_TRY(check_layer(layer));
-  POETX_TRY(check_ptr(W0lin));
-  int dev;
-  POETX_TRY(current_device(&dev));
-  const poetx_layer& L = *layer;
-  // W[j'][i'] = W0lin[permP[j']][permR[i']]
-  POETX_CUDA(gather_dt(L.dtype, W0lin, L.m, L.n, L.W, L.m, L.n, L.m, L.permR, L.permP,
-                       static_cast<cudaStream_t>(stream), dev));
-  return POETX_OK;
-}
-
-poetx_status poetx_frame_export(const poetx_layer* layer, void* W0lin, void* stream) {
-  POETX_TRY(check_layer(layer));
-  POETX_TRY(check_ptr(W0lin));
-  int dev;
-  POETX_TRY(current_device(&dev));
-  const poetx_layer& L = *layer;
-  // W0lin[permP[j']][permR[i']] = W[j'][i']
-  POETX_CUDA(scatter_dt(L.dtype, L.W, L.m, W0lin, L.m, L.n, L.n, L.m, L.permR, L.permP,
-                        static_cast<cudaStream_t>(stream), dev));
-  return POETX_OK;
-}
-
-poetx_status poetx_cnp_build(int32_t nblk, int32_t b, const float* q, int32_t dtype, void* G, void* ws,
-                             size_t ws_bytes, void* stream) {
-  POETX_TRY(check_dtype_b(dtype, b));
-  if (nblk < 0) return POETX_E_ARG;
-  if (nblk == 0) return POETX_OK;
-  POETX_TRY(check_ptr(q));
-  POETX_TRY(check_ptr(G));
-  if (!ws || ws_bytes < poetx_cnp_workspace_bytes(nblk, b, dtype)) return POETX_E_WORKSPACE;
-  int dev;
-  POETX_TRY(current_device(&dev));
-  Carver c(ws, ws_bytes);
-  return cnp_build2(b, dtype, q, nblk, G, nullptr, 0, nullptr, c, static_cast<cudaStream_t>(stream), dev);
-}
-
-poetx_status poetx_cnp_backward(int32_t nblk, int32_t b, const float* q, const float* dG, float* dq,
-                                int32_t accumulate, int32_t dtype, void* ws, size_t ws_bytes, void* stream) {
-  POETX_TRY(check_dtype_b(dtype, b));
-  if (nblk < 0) return POETX_E_ARG;
-  if (nblk == 0) return POETX_OK;
-  POETX_TRY(check_ptr(q));
-  POETX_TRY(check_ptr(dG));
-  POETX_TRY(check_ptr(dq));
-  if (!ws || ws_bytes < poetx_cnp_workspace_bytes(nblk, b, dtype)) return POETX_E_WORKSPACE;
-  int dev;
-  POETX_TRY(current_device(&dev));
-  Carver c(ws, ws_bytes);
-  return cnp_backward2(b, dtype, q, nblk, dG, 1, dq, nullptr, 0, nullptr, 1, nullptr, accumulate, c,
-                       static_cast<cudaStream_t>(stream), dev);
-}
-
-poetx_status poetx_forward(const poetx_layer* layer, int64_t T, const void* x, void* z, void* y_save,
-                           void* xg_save, void* ws, size_t ws_bytes, void* stream) {
-  POETX_TRY(check_layer(layer));
-  if (T < 0) return POETX_E_ARG;
-  if (T > kMaxT) return POETX_E_SHAPE;
-  if (T == 0) return POETX_OK;
-  POETX_TRY(check_ptr(x));
-  POETX_TRY(check_ptr(z));
-  if (y_save && !aligned16(y_save)) return POETX_E_ALIGN;
-  if (xg_save && !aligned16(xg_save)) return POETX_E_ALIGN;
-  if (!ws || ws_bytes < fwd_ws(layer, T)) return POETX_E_WORKSPACE;
-  int dev;
-  POETX_TRY(current_device(&dev));
-  const poetx_layer& L = *layer;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int et = elem_type(L.dtype);
-  const size_t es = dtype_size(L.dtype);
-  const bool tc_path = use_tc(L.dtype);
-  if (!y_save && !xg_save && weight_centric_forward(L, T)) {
-    // two [n][m] weights fit in the workspace whenever this path is chosen
-    Carver cw(ws, ws_bytes);
-    if (cw.fits(2 * al(es * size_t(L.n) * L.m))) {
-      void* W1 = cw.take<uint8_t>(es * size_t(L.n) * L.m);
-      void* W2 = cw.take<uint8_t>(es * size_t(L.n) * L.m);
-      // W1 = W~ Diag(G_R)^T, W2 = Diag(G_P)^T W1, W1 = W2 in natural order
-      PROFILED(ST_BLOCKDIAG, st,
-               POETX_CUDA(launch_gemm(blockdiag_desc(L.W, et, L.n, L.m, L.b, L.GR, true, W1, et), tc_path, st, dev)));
-      POETX_CUDA(fold_p_rows(L, W1, W2, st, dev));
-      PROFILED(ST_PERMUTE, st,
-               POETX_CUDA(scatter_dt(L.dtype, W2, L.m, W1, L.m, L.n, L.n, L.m, L.permR, L.permP, st, dev)));
-      // z = x W1^T
-      GemmDesc g;
-      g.M = static_cast<int>(T);
-      g.N = L.n;
-      g.K = L.m;
-      g.A = colblocks_view(x, et, T, L.m, 0);
-      Operand2D b;
-      b.ptr = W1;
-      b.et = et;
-      b.rows = L.n;
-      b.cols = L.m;
-      b.ld = L.m;
-      b.mn_major = false;
-      g.B = b;
-      g.C.ptr = z;
-      g.C.et = et;
-      g.C.ld = L.n;
-      g.C.view_rows = T;
-      g.C.view_cols = L.n;
-      PROFILED(ST_W0, st, POETX_CUDA(launch_gemm(g, tc_path, st, dev)));
-      return POETX_OK;
-    }
-  }
-  Carver c(ws, ws_bytes);
-  void* Xw = c.take<uint8_t>(es * T * L.m);
-  void* Xg = xg_save ? xg_save : Xw;
-  void* U = c.take<uint8_t>(es * T * L.m);
-  void* V = c.take<uint8_t>(es * T * L.n);
-  void* Yw = c.take<uint8_t>(es * T * L.n);
-  void* Y = y_save ? y_save : Yw;
-  // Xg = x Psi_R^T  (columns gathered into the Psi_R frame)
-  PROFILED(ST_PERMUTE, st, POETX_CUDA(permute_dt(L.dtype, x, Xg, T, L.m, L.permR, 0, st, dev)));
-  // Y = (Xg Diag(G_R)) W~^T  (W~ = Psi_R W0 Psi_P^T stored [n][m]); U in `U`, or,
-  // with POETX_FOLD_R and T > n, the weight with G_R folded in
-  POETX_CUDA(y_from_xg(L, T, Xg, Y, U, st, dev));
-  // V_j = Y_j G_Pj
-  PROFILED(ST_BLOCKDIAG, st, POETX_CUDA(launch_gemm(blockdiag_desc(Y, et, T, L.n, L.b, L.GP, false, V, et), tc_path, st, dev)));
-  // z = V Psi_P  (columns scattered back to natural order)
-  PROFILED(ST_PERMUTE, st, POETX_CUDA(permute_dt(L.dtype, V, z, T, L.n, L.permP, 1, st, dev)));
-  return POETX_OK;
-}
-
-// Backward of one layer.  Gradient mode "dq" (dGR == dGP == NULL): the
-// packed dq of both sides through the CNP backward.  Mode "dG" (dqR == dqP
-// == NULL): the token sums dG of both sides, CNP backward left to the caller.
-static poetx_status backward_impl(const poetx_layer* layer, int64_t T, const void* x, const void* y_save,
-                           const void* xg_save, const void* dz, void* dx, float* dqR, float* dqP, float* dGR,
-                           float* dGP, int32_t accumulate, void* ws, size_t ws_bytes, void* stream) {
-  POETX_TRY(check_layer(layer));
-  if (T < 0) return POETX_E_ARG;
-  if (T > kMaxT) return POETX_E_SHAPE;
-  const bool dg_mode = dGR != nullptr;
-  const poetx_layer& L = *layer;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int nR = L.m / L.b, nP = L.n / L.b;
-  const size_t outR = dg_mode ? size_t(nR) * L.b * L.b : size_t(nR) * L.b * (L.b - 1) / 2;
-  const size_t outP = dg_mode ? size_t(nP) * L.b * L.b : size_t(nP) * L.b * (L.b - 1) / 2;
-  float* oR = dg_mode ? dGR : dqR;
-  float* oP = dg_mode ? dGP : dqP;
-  if (T == 0) {
-    if (!accumulate) {
-      POETX_CUDA(cudaMemsetAsync(oR, 0, sizeof(float) * outR, st));
-      POETX_CUDA(cudaMemsetAsync(oP, 0, sizeof(float) * outP, st));
-    }
-    return POETX_OK;
-  }
-  if (!xg_save) POETX_TRY(check_ptr(x));
-  if (y_save && !aligned16(y_save)) return POETX_E_ALIGN;
-  POETX_TRY(check_ptr(dz));
-  if (xg_save && !aligned16(xg_save)) return POETX_E_ALIGN;
-  if (dx && !aligned16(dx)) return POETX_E_ALIGN;
-  const bool recompute = y_save == nullptr;
-  if (!ws || ws_bytes < (recompute ? bwd_recompute_ws(layer, T) : bwd_ws(layer, T))) return POETX_E_WORKSPACE;
-  int dev;
-  POETX_TRY(current_device(&dev));
-  const int et = elem_type(L.dtype);
-  const size_t es = dtype_size(L.dtype);
-  const bool tc_path = use_tc(L.dtype);
-  const int64_t mx = L.m > L.n ? L.m : L.n;
-  const size_t bb = size_t(L.b) * L.b;
-  const int sP = dg_splits(nP, L.b, T, L.dtype), sR = dg_splits(nR, L.b, T, L.dtype);
-  Carver c(ws, ws_bytes);
-  void* bufA = c.take<uint8_t>(es * T * mx);
-  void* bufB = c.take<uint8_t>(es * T * mx);
-  void* dU = c.take<uint8_t>(es * T * L.m);
-  float* partP = c.take<float>(sizeof(float) * sP * nP * bb);
-  float* partR = c.take<float>(sizeof(float) * sR * nR * bb);
-  // dG mode: a single split without accumulation goes straight to dG
-  if (dg_mode && !accumulate && sP == 1) partP = dGP;
-  if (dg_mode && !accumulate && sR == 1) partR = dGR;
-
-  if (recompute) {
-    // "mem" variant: Y was not kept; recompute it from x (Xg, then Y as in the forward)
-    void* Ybuf = c.take<uint8_t>(es * T * L.n);
-    void* Xbuf = c.take<uint8_t>(es * T * L.m);
-    if (!xg_save) {
-      PROFILED(ST_PERMUTE, st, POETX_CUDA(permute_dt(L.dtype, x, Xbuf, T, L.m, L.permR, 0, st, dev)));
-      xg_save = Xbuf;
-    }
-    // the forward's Y, by the same arithmetic (dU, written only later, holds U or the folded weight)
-    POETX_CUDA(y_from_xg(L, T, xg_save, Ybuf, dU, st, dev));
-    y_save = Ybuf;
-  }
-
-  // dV = dz Psi_P^T
-  void* dV = bufA;
-  PROFILED(ST_PERMUTE, st, POETX_CUDA(permute_dt(L.dtype, dz, dV, T, L.n, L.permP, 0, st, dev)));
-  // dY_j = dV_j G_Pj^T and dG_Pj = Y_j^T dV_j (split over tokens): one kernel
-  // reading dV once (b = 256 bf16), else two GEMMs.  With POETX_FOLD_P and
-  // T > m (bf16) dY is not formed at all: G_P is folded into the weight (W_P = Diag(G_P)^T W~,
-  // [n][m], one weight-sized pass) and dU = dV W_P below, so only the dG
-  // product reads dV here.
-  void* dY = bufB;
-  const bool fold_p = fold_p_into_weight(L, T);
-  if (fold_p) {
-    POETX_CUDA(fold_p_rows(L, L.W, bufB, st, dev));
-    PROFILED(ST_DG, st, POETX_CUDA(launch_gemm(blockgrad_desc(y_save, dV, et, T, L.n, L.b, sP, partP), tc_path, st, dev)));
-  } else if (use_pair_bdg(L)) {
-    PROFILED(ST_BDG, st, POETX_CUDA(launch_bdg(dV, y_save, L.GP, dY, partP, T, L.n, sP, st, dev)));
-  } else {
-    PROFILED(ST_BLOCKDIAG, st, POETX_CUDA(launch_gemm(blockdiag_desc(dV, et, T, L.n, L.b, L.GP, true, dY, et), tc_path, st, dev)));
-    PROFILED(ST_DG, st, POETX_CUDA(launch_gemm(blockgrad_desc(y_save, dV, et, T, L.n, L.b, sP, partP), tc_path, st, dev)));
-  }
-  // dU = dY W~^T  (B(k=j', n=i') = W[j'][i'], MN-major), or dU = dV W_P
-  {
-    GemmDesc g;
-    g.M = static_cast<int>(T);
-    g.N = L.m;
-    g.K = L.n;
-    g.A = colblocks_view(fold_p ? dV : dY, et, T, L.n, 0);
-    Operand2D b;
-    b.ptr = fold_p ? bufB : L.W;
-    b.et = et;
-    b.rows = L.n;
-    b.cols = L.m;
-    b.ld = L.m;
-    b.mn_major = true;
-    g.B = b;
-    g.C.ptr = dU;
-    g.C.et = et;
-    g.C.ld = L.m;
-    g.C.view_rows = T;
-    g.C.view_cols = L.m;
-    PROFILED(ST_W0, st, POETX_CUDA(launch_gemm(g, tc_path, st, dev)));
-  }
-  // Xg = x Psi_R^T: the forward's copy when it saved one, else re-gathered (dV is dead)
-  const void* Xg = xg_save;
-  if (!Xg) {
-    Xg = bufA;
-    PROFILED(ST_PERMUTE, st, POETX_CUDA(permute_dt(L.dtype, x, bufA, T, L.m, L.permR, 0, st, dev)));
-  }
-  // dXg_j = dU_j G_Rj^T (dY is dead; only with dx) and dG_Rj = Xg_j^T dU_j
-  void* dXg = bufB;
-  if (use_pair_bdg(L)) {
-    PROFILED(ST_BDG, st, POETX_CUDA(launch_bdg(dU, Xg, L.GR, dx ? dXg : nullptr, partR, T, L.m, sR, st, dev)));
-  } else {
-    if (dx) PROFILED(ST_BLOCKDIAG, st, POETX_CUDA(launch_gemm(blockdiag_desc(dU, et, T, L.m, L.b, L.GR, true, dXg, et), tc_path, st, dev)));
-    PROFILED(ST_DG, st, POETX_CUDA(launch_gemm(blockgrad_desc(Xg, dU, et, T, L.m, L.b, sR, partR), tc_path, st, dev)));
-  }
-  // dx = dXg Psi_R
-  if (dx) PROFILED(ST_PERMUTE, st, POETX_CUDA(permute_dt(L.dtype, dXg, dx, T, L.m, L.permR, 1, st, dev)));
-  if (dg_mode) {
-    // dG = fixed-order sum of the token splits (skipped when the GEMM wrote dG)
-    const bool sumP = partP != dGP, sumR = partR != dGR;
-    if (sumP || sumR) {
-      const int64_t n4P = sumP ? int64_t(nP) * int64_t(bb) / 4 : 0;
-      const int64_t n4R = sumR ? int64_t(nR) * int64_t(bb) / 4 : 0;
-      PROFILED(ST_REDUCE, st,
-               sum_splits2_kernel<<<grid_for(n4P + n4R, 256, dev), 256, 0, st>>>(
-                   reinterpret_cast<const float4*>(partP), sP, n4P, reinterpret_cast<float4*>(dGP),
-                   reinterpret_cast<const float4*>(partR), sR, n4R, reinterpret_cast<float4*>(dGR), accumulate));
-      POETX_CUDA(cudaGetLastError());
-    }
-    return POETX_OK;
-  }
-  // dq from the dG partial sums of both sides (fixed-order reduction of the
-  // token splits inside the CNP backward)
-  POETX_TRY(cnp_backward2(L.b, L.dtype, L.qP, nP, partP, sP, dqP, L.qR, nR, partR, sR, dqR, accumulate, c, st, dev));
-  return POETX_OK;
-}
-
-poetx_status poetx_backward(const poetx_layer* layer, int64_t T, const void* x, const void* y_save,
-                            const void* xg_save, const void* dz, void* dx, float* dqR, float* dqP,
-                            int32_t accumulate, void* ws, size_t ws_bytes, void* stream) {
-  POETX_TRY(check_ptr(dqR));
-  POETX_TRY(check_ptr(dqP));
-  return backward_impl(layer, T, x, y_save, xg_save, dz, dx, dqR, dqP, nullptr, nullptr, accumulate, ws, ws_bytes,
-                       stream);
-}
-
-poetx_status poetx_backward_dG(const poetx_layer* layer, int64_t T, const void* x, const void* y_save,
-                               const void* xg_save, const void* dz, void* dx, float* dGR, float* dGP,
-                               int32_t accumulate, void* ws, size_t ws_bytes, void* stream) {
-  POETX_TRY(check_ptr(dGR));
-  POETX_TRY(check_ptr(dGP));
-  return backward_impl(layer, T, x, y_save, xg_save, dz, dx, nullptr, nullptr, dGR, dGP, accumulate, ws, ws_bytes,
-                       stream);
-}
-
-poetx_status poetx_merge(const poetx_layer* layer, const int32_t* new_permR, const int32_t* new_permP,
-                         void* W_out, void* ws, size_t ws_bytes, void* stream) {
-  POETX_TRY(check_layer(layer));
-  POETX_TRY(check_ptr(new_permR));
-  POETX_TRY(check_ptr(new_permP));
-  POETX_TRY(check_ptr(W_out));
-  const poetx_layer& L = *layer;
-  const size_t es = dtype_size(L.dtype);
-  const size_t wbytes = es * size_t(L.n) * L.m;
-  {
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(L.W), b0 = reinterpret_cast<uintptr_t>(W_out);
-    if (a0 < b0 + wbytes && b0 < a0 + wbytes) return POETX_E_ARG;
-  }
-  if (!ws || ws_bytes < merge_ws(layer)) return POETX_E_WORKSPACE;
-  int dev;
-  POETX_TRY(current_device(&dev));
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int et = elem_type(L.dtype);
-  const bool tc_path = use_tc(L.dtype);
-  const int nR = L.m / L.b, nP = L.n / L.b;
-  const size_t nm = size_t(L.n) * L.m;
-  Carver c(ws, ws_bytes);
-  float* B1t = c.take<float>(sizeof(float) * nm);
-  float* At = c.take<float>(sizeof(float) * nm);
-  float* GPt = c.take<float>(sizeof(float) * size_t(nP) * L.b * L.b);
-  int32_t* invR = c.take<int32_t>(sizeof(int32_t) * L.m);
-  int32_t* invP = c.take<int32_t>(sizeof(int32_t) * L.n);
-  int32_t* sigR = c.take<int32_t>(sizeof(int32_t) * L.m);
-  int32_t* sigP = c.take<int32_t>(sizeof(int32_t) * L.n);
-
-  // Stored W~ = (Psi_R W0 Psi_P^T)^T.  New weight R W0 P in the old frame is
-  // A' = Diag(G_R) W~ Diag(G_P), stored transposed:
-  //   At = Diag(G_P)^T . W . Diag(G_R)^T     ([n][m])
-  // pass 1: B1t = Diag(G_R) . W^T ([m][n]); block i: B1t[ib + r][c] = sum_k G_Ri[r][k] W[c][ib + k]
-  {
-    GemmDesc g;
-    g.M = L.b;
-    g.N = L.n;
-    g.K = L.b;
-    g.batch = nR;
-    g.A = blocks_view(L.GR, et, nR, L.b, true);          // A(r, k) = G_Ri[r][k]
-    g.B = colblocks_view(L.W, et, L.n, L.m, L.b);        // B(k, c) = W[c][ib + k]
-    g.C.ptr = B1t;
-    g.C.et = ET_F32;
-    g.C.ld = L.n;
-    g.C.batch_stride = int64_t(L.b) * L.n;
-    g.C.view_rows = L.m;
-    g.C.view_cols = L.n;
-    g.C.b_row = L.b;
-    PROFILED(ST_MERGE, st, POETX_CUDA(launch_gemm(g, tc_path, st, dev)));
-  }
-  // pass 2: At[jb + r][c] = sum_k G_Pj[k][r] B1t[c][jb + k]  (G_Pj^T, fp32, K-major)
-  {
-    const dim3 tgrid((L.b + 31) / 32, (L.b + 31) / 32, nP), tblock(32, 8);
-    if (L.dtype == POETX_BF16)
-      PROFILED(ST_MERGE, st, transpose_blocks_kernel<<<tgrid, tblock, 0, st>>>(
-                                 static_cast<const __nv_bfloat16*>(L.GP), GPt, L.b));
-    else
-      PROFILED(ST_MERGE, st,
-               transpose_blocks_kernel<<<tgrid, tblock, 0, st>>>(static_cast<const float*>(L.GP), GPt, L.b));
-    POETX_CUDA(cudaGetLastError());
-    GemmDesc g;
-    g.M = L.b;
-    g.N = L.m;
-    g.K = L.b;
-    g.batch = nP;
-    g.A = blocks_view(GPt, ET_F32, nP, L.b, true);       // A(r, k) = G_Pj[k][r]
-    g.B = colblocks_view(B1t, ET_F32, L.m, L.n, L.b);    // B(k, c) = B1t[c][jb + k]
-    g.C.ptr = At;
-    g.C.et = ET_F32;
-    g.C.ld = L.m;
-    g.C.batch_stride = int64_t(L.b) * L.m;
-    g.C.view_rows = L.n;
-    g.C.view_cols = L.m;
-    g.C.b_row = L.b;
-    PROFILED(ST_MERGE, st, POETX_CUDA(launch_gemm(g, tc_path, st, dev)));
-  }
-  // New frame: W'[j'][i'] = At[sigP[j']][sigR[i']], sig = perm_old^-1 o perm_new.
-  invert_perm_kernel<<<(L.m + 255) / 256, 256, 0, st>>>(L.permR, invR, L.m);
-  invert_perm_kernel<<<(L.n + 255) / 256, 256, 0, st>>>(L.permP, invP, L.n);
-  compose_perm_kernel<<<(L.m + 255) / 256, 256, 0, st>>>(invR, new_permR, sigR, L.m);
-  compose_perm_kernel<<<(L.n + 255) / 256, 256, 0, st>>>(invP, new_permP, sigP, L.n);
-  POETX_CUDA(cudaGetLastError());
-  if (L.dtype == POETX_BF16)
-    POETX_CUDA(gather(static_cast<const float*>(At), L.m, L.n, static_cast<__nv_bfloat16*>(W_out), L.m, L.n, L.m,
-                      sigR, sigP, st, dev));
-  else
-    POETX_CUDA(gather(static_cast<const float*>(At), L.m, L.n, static_cast<float*>(W_out), L.m, L.n, L.m, sigR, sigP,
-                      st, dev));
-  // Reset: Q = 0, G = I.
-  POETX_CUDA(cudaMemsetAsync(L.qR, 0, sizeof(float) * size_t(nR) * L.b * (L.b - 1) / 2, st));
-  POETX_CUDA(cudaMemsetAsync(L.qP, 0, sizeof(float) * size_t(nP) * L.b * (L.b - 1) / 2, st));
-  const int64_t cR = int64_t(nR) * L.b * L.b, cP = int64_t(nP) * L.b * L.b;
-  if (L.dtype == POETX_BF16) {
-    identity_blocks_kernel<__nv_bfloat16>
-        <<<grid_for(cR, 256, dev), 256, 0, st>>>(static_cast<__nv_bfloat16*>(L.GR), nR, L.b);
-    identity_blocks_kernel<__nv_bfloat16>
-        <<<grid_for(cP, 256, dev), 256, 0, st>>>(static_cast<__nv_bfloat16*>(L.GP), nP, L.b);
-  } else {
-    identity_blocks_kernel<float><<<grid_for(cR, 256, dev), 256, 0, st>>>(static_cast<float*>(L.GR), nR, L.b);
-    identity_blocks_kernel<float><<<grid_for(cP, 256, dev), 256, 0, st>>>(static_cast<float*>(L.GP), nP, L.b);
-  }
-  POETX_CUDA(cudaGetLastError());
-  return POETX_OK;
-}
-
-poetx_status poetx_check_perm(const int32_t* perm, int32_t len, int32_t* d_ok, void* ws, size_t ws_bytes,
-                              void* stream) {
-  if (len <= 0) return POETX_E_ARG;
-  POETX_TRY(check_ptr(perm));
-  if (!d_ok) return POETX_E_ARG;
-  if (!ws || ws_bytes < poetx_check_perm_workspace_bytes(len)) return POETX_E_WORKSPACE;
-  int dev;
-  POETX_TRY(current_device(&dev));
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  Carver c(ws, ws_bytes);
-  int32_t* hist = c.take<int32_t>(sizeof(int32_t) * len);
-  POETX_CUDA(cudaMemsetAsync(hist, 0, sizeof(int32_t) * len, st));
-  set_int_kernel<<<1, 1, 0, st>>>(d_ok, 1);
-  perm_histogram_kernel<<<(len + 255) / 256, 256, 0, st>>>(perm, hist, len, d_ok);
-  perm_check_kernel<<<(len + 255) / 256, 256, 0, st>>>(hist, len, d_ok);
-  POETX_CUDA(cudaGetLastError());
-  return POETX_OK;
-}
-
-int32_t poetx_profile_stage_count(void) { return ST_COUNT; }
-
-const char* poetx_profile_stage_name(int32_t stage) {
-  if (stage < 0 || stage >= ST_COUNT) return "unknown";
-  return kStageNames[stage];
-}
-
-poetx_status poetx_profile_begin(void) {
-  Profiler& P = profiler();
-  std::lock_guard<std::mutex> g(P.mu);
-  P.on = true;
-  P.used = 0;
-  P.recs.clear();
-  P.done.clear();
-  return POETX_OK;
-}
-
-poetx_status poetx_profile_end(double* ms_per_stage, int64_t* launches_per_stage, int32_t nstages) {
-  if (!ms_per_stage || !launches_per_stage || nstages < 0) return POETX_E_ARG;
-  Profiler& P = profiler();
-  std::lock_guard<std::mutex> g(P.mu);
-  for (int i = 0; i < nstages; ++i) {
-    ms_per_stage[i] = 0.0;
-    launches_per_stage[i] = 0;
-  }
-  poetx_status st = POETX_OK;
-  for (const auto& r : P.recs) {
-    if (cudaEventSynchronize(P.pool[r.second + 1]) != cudaSuccess) {
-      (void)cudaGetLastError();
-      st = POETX_E_CUDA;
-      break;
-    }
-    float ms = 0.f;
-    if (cudaEventElapsedTime(&ms, P.pool[r.second], P.pool[r.second + 1]) != cudaSuccess) {
-      (void)cudaGetLastError();
-      st = POETX_E_CUDA;
-      break;
-    }
-    if (r.first < nstages) {
-      ms_per_stage[r.first] += ms;
-      launches_per_stage[r.first] += 1;
-    }
-    P.done.emplace_back(r.first, ms);
-  }
-  P.on = false;
-  P.used = 0;
-  P.recs.clear();
-  return st;
-}
-
-int32_t poetx_profile_records(int32_t* stages, float* ms, int32_t max_records) {
-  Profiler& P = profiler();
-  std::lock_guard<std::mutex> g(P.mu);
-  const int32_t n = static_cast<int32_t>(P.done.size());
-  if (!stages || !ms || max_records <= 0) return n;
-  const int32_t k = n < max_records ? n : max_records;
-  for (int32_t i = 0; i < k; ++i) {
-    stages[i] = P.done[i].first;
-    ms[i] = P.done[i].second;
-  }
-  return n;
-}
-
-}  // extern "C"
-
-// ---------------------------------------------------------------- fixed-scratch CNP build
-// Some callers cannot allocate device memory when they build G: a host
-// program that links only this C library and has no device allocator of its
-// own, or a serving process that reserves its whole memory budget at start-up
-// and forbids allocations afterwards.  For them poetx_cnp_build_fixed takes
-// its scratch (Q, S and H for every block) from this file-scope device array
-// instead of a caller workspace.  The array is kFixedScratchBytes on every
-// GPU that loads the library, for the life of the process: b = 256 bf16
-// builds of up to 47 blocks (the pair kernel takes 128 KiB per block plus
-// three per pair of SMs), other builds of up to ~2.09e6 fp32 elements of Q
-// (b = 512: 7 blocks).  Host code must
-// not hand the symbol itself to a kernel (on the host it only names the
-// array); the device address comes from cudaGetSymbolAddress, looked up once
-// per device on that device's first call.
-constexpr size_t kFixedScratchBytes = size_t(24) << 20;
-static __device__ __align__(256) unsigned char g_cnp_fixed_scratch[kFixedScratchBytes];
-
+// ---------------------------------------------------------------- 8-bit path
 namespace {
-std::mutex g_fixed_mu;
-void* g_fixed_scratch_ptr[64] = {nullptr};
 
-// Device address of the fixed scratch on the current device `dev`.
-poetx_status fixed_scratch(int dev, void** out) {
-  std::lock_guard<std::mutex> g(g_fixed_mu);
-  if (!g_fixed_scratch_ptr[dev]) {
-    void* p = nullptr;
-    if (cudaGetSymbolAddress(&p, g_cnp_fixed_scratch) != cudaSuccess || !p) {
-      (void)cudaGetLastError();
-      return POETX_E_CUDA;
-    }
-    g_fixed_scratch_ptr[dev] = p;
-  }
-  *out = g_fixed_scratch_ptr[dev];
-  return POETX_OK;
-}
-}  // namespace
-
-extern "C" poetx_status poetx_cnp_build_fixed(int32_t nblk, int32_t b, const float* q, int32_t dtype, void* G,
-                                              void* stream) {
-  POETX_TRY(check_dtype_b(dtype, b));
-  if (nblk < 0) return POETX_E_ARG;
-  if (nblk == 0) return POETX_OK;
-  POETX_TRY(check_ptr(q));
-  POETX_TRY(check_ptr(G));
-  int dev;
-  POETX_TRY(current_device(&dev));
-  // the scratch the build will carve: the fused pair kernel's bf16 operand
-  // region (b = 256 bf16), else Q, S and H in fp32 for every block; requests
-  // that do not fit are refused before anything is queued
-  const size_t need = kAlign + (use_pair_cnp(b, dtype) ? cnp_pair_bytes(nblk, false, false, dev)
-                                                       : 3 * cnp_units(nblk, b));
-  if (need > kFixedScratchBytes) return POETX_E_WORKSPACE;  // too many blocks for the fixed scratch
-  void* scratch = nullptr;
-  POETX_TRY(fixed_scratch(dev, &scratch));
-  // Every scratch matrix (Q, S, H, or the pair kernel's bf16 operands) is
-  // written in full before it is read: nothing to clear.
-  Carver c(scratch, kFixedScratchBytes);
-  return cnp_build2(b, dtype, q, nblk, G, nullptr, 0, nullptr, c, static_cast<cudaStream_t>(stream), dev);
-}
-
-// ---------------------------------------------------------------- failure-path self-test
-// One warp waits on an mbarrier that no thread ever arrives on, through the
-// same bounded wait the GEMM and copy kernels use, with a short limit: the
-// wait gives up, records DERR_GEMM_WAIT in the sticky error word and the
-// kernel returns normally.  No copy, MMA or TMEM allocation is involved, so
-// nothing is left in flight.  out[0] = 1 if the wait ended by an arrival
-// (never expected), out[1] = nanoseconds waited.
-namespace {
-__global__ void stalled_wait_kernel(uint64_t limit_ns, unsigned long long* out) {
-  __shared__ __align__(8) uint64_t bar;
-  if (threadIdx.x == 0) {
-    mbar_init(smem_u32(&bar), 1);
-    fence_barrier_init();
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    const uint64_t t0 = global_ns();
-    const bool arrived = mbar_wait_for(smem_u32(&bar), 0, DERR_GEMM_WAIT, limit_ns);
-    out[0] = arrived ? 1ull : 0ull;
-    out[1] = global_ns() - t0;
-  }
-}
-}  // namespace
-
-extern "C" poetx_status poetx_selftest_wait_timeout(uint32_t limit_us, unsigned long long* d_out, void* stream) {
-  if (limit_us < 1 || limit_us > 1000000) return POETX_E_ARG;
-  if (!d_out) return POETX_E_ARG;
-  if (reinterpret_cast<uintptr_t>(d_out) & 7u) return POETX_E_ALIGN;
-  int dev;
-  POETX_TRY(current_device(&dev));
-  stalled_wait_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(uint64_t(limit_us) * 1000ull, d_out);
-  POETX_CUDA(cudaGetLastError());
-  return POETX_OK;
-}
-
-// ---------------------------------------------------------------- POET-XQ weight storage
-namespace {
 // Calls f with the columns a lane takes in the checkpoint and expansion
 // kernels (see there) and their grid.
 template <typename T, bool SAVE, typename F>
@@ -1736,69 +1047,6 @@ cudaError_t launch_expand(const int8_t* codes, const uint8_t* exps, const float*
     return cudaGetLastError();
   });
 }
-}  // namespace
-
-extern "C" poetx_status poetx_weight_quantize(int32_t n, int32_t m, const void* W, int32_t dtype, int8_t* Wq,
-                                              float* scale, void* stream) {
-  if (dtype != POETX_FP32 && dtype != POETX_BF16) return POETX_E_DTYPE;
-  if (n < 0 || m <= 0) return POETX_E_ARG;
-  if (n == 0) return POETX_OK;
-  POETX_TRY(check_ptr(W));
-  POETX_TRY(check_ptr(Wq));
-  POETX_TRY(check_ptr(scale));
-  int dev;
-  POETX_TRY(current_device(&dev));
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int grid = n < sm_count(dev) * 8 ? n : sm_count(dev) * 8;
-  if (dtype == POETX_BF16)
-    quantize_rows_kernel<<<grid, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(W), n, m, Wq, scale);
-  else
-    quantize_rows_kernel<<<grid, 256, 0, st>>>(static_cast<const float*>(W), n, m, Wq, scale);
-  POETX_CUDA(cudaGetLastError());
-  return POETX_OK;
-}
-
-extern "C" poetx_status poetx_weight_dequantize(int32_t n, int32_t m, const int8_t* Wq, const float* scale,
-                                                int32_t dtype, void* W, void* stream) {
-  if (dtype != POETX_FP32 && dtype != POETX_BF16) return POETX_E_DTYPE;
-  if (n < 0 || m <= 0) return POETX_E_ARG;
-  if (n == 0) return POETX_OK;
-  POETX_TRY(check_ptr(W));
-  POETX_TRY(check_ptr(Wq));
-  POETX_TRY(check_ptr(scale));
-  int dev;
-  POETX_TRY(current_device(&dev));
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  PROFILED(ST_DEQUANT, st,
-           POETX_CUDA(dtype == POETX_BF16 ? launch_expand<__nv_bfloat16>(Wq, nullptr, scale, n, m, W, st, dev)
-                                          : launch_expand<float>(Wq, nullptr, scale, n, m, W, st, dev)));
-  return POETX_OK;
-}
-
-// ---------------------------------------------------------------- optimizer step on packed q
-extern "C" poetx_status poetx_adamw_step(int64_t n, float* q, const float* grad, float* m1, float* m2, float lr,
-                                         float beta1, float beta2, float eps, float weight_decay, int32_t step,
-                                         void* stream) {
-  if (n < 0 || step < 1) return POETX_E_ARG;
-  if (n == 0) return POETX_OK;
-  POETX_TRY(check_ptr(q));
-  POETX_TRY(check_ptr(grad));
-  POETX_TRY(check_ptr(m1));
-  POETX_TRY(check_ptr(m2));
-  int dev;
-  POETX_TRY(current_device(&dev));
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const float bc1 = static_cast<float>(1.0 - std::pow(static_cast<double>(beta1), step));
-  const float bc2 = static_cast<float>(1.0 - std::pow(static_cast<double>(beta2), step));
-  PROFILED(ST_OPTIM, st,
-           adamw_kernel<<<grid_for((n + 3) / 4, 256, dev), 256, 0, st>>>(n, q, grad, m1, m2, lr, beta1, beta2, eps,
-                                                                         weight_decay, bc1, bc2));
-  POETX_CUDA(cudaGetLastError());
-  return POETX_OK;
-}
-
-// ======================================================================== 8-bit path
-namespace {
 
 constexpr int32_t kMaxD8 = 102400;  // widest row: |code| <= 128 keeps a sum of that many products below 2^31
 
@@ -2272,6 +1520,937 @@ poetx_status check_block(int64_t T, int32_t d, int32_t b, int32_t dtype) {
 
 }  // namespace
 
+// ---- the layer's forward and backward in 8 bits
+namespace {
+
+poetx_status check_q8(const poetx_layer* layer, const poetx_q8* q) {
+  POETX_TRY(check_layer(layer));
+  if (!q) return POETX_E_ARG;
+  if (layer->fold) return POETX_E_ARG;  // the folded forms read the weight itself
+  if (!q->Wq != !q->wscale || !q->y_codes != !q->y_exps || !q->xg_codes != !q->xg_exps) return POETX_E_ARG;
+  const void* ptrs[] = {q->Wq, q->wscale, q->y_codes, q->y_exps, q->xg_codes, q->xg_exps};
+  for (const void* p : ptrs) POETX_TRY(check_opt(p));
+  return POETX_OK;
+}
+
+// int8 rows of the W0 products: U's, or dY's (and the weight with padded rows)
+size_t i8_layer_ws(const poetx_layer* L, int64_t T, bool backward) {
+  return al(size_t(T) * row16(backward ? L->n : L->m)) + al(sizeof(float) * size_t(T)) +
+         (L->m % 16 ? al(size_t(L->n) * row16(L->m)) : 0);
+}
+
+size_t fwd_q8_ws(const poetx_layer* L, int64_t T, const poetx_q8& q) {
+  return fwd_ws(L, T) + (q.Wq ? i8_layer_ws(L, T, false) : 0);
+}
+
+bool expands_checkpoint(const poetx_layer& L) { return L.dtype == POETX_BF16 && !use_pair_bdg8(L.b, L.dtype); }
+
+size_t bwd_q8_ws(const poetx_layer* L, int64_t T, const poetx_q8& q, bool recompute) {
+  const size_t es = dtype_size(L->dtype);
+  const int64_t mx = L->m > L->n ? L->m : L->n;
+  size_t need = recompute ? bwd_recompute_ws(L, T) : bwd_ws(L, T);
+  // partial sums by the checkpoint kernels' own splits
+  if (q.y_codes) need += al(sizeof(float) * size_t(block_backward_splits(T, L->n, L->b, L->dtype)) * L->n * L->b);
+  if (q.xg_codes) need += al(sizeof(float) * size_t(block_backward_splits(T, L->m, L->b, L->dtype)) * L->m * L->b);
+  if ((q.y_codes || q.xg_codes) && expands_checkpoint(*L)) need += al(es * T * mx);
+  if (q.Wq) {
+    const size_t f = recompute ? i8_layer_ws(L, T, false) : 0, g = i8_layer_ws(L, T, true);
+    need += f > g ? f : g;
+  }
+  return need;
+}
+
+// Wq with rows TMA can read (copied when m is no multiple of 16).
+cudaError_t weight_rows(const poetx_layer& L, const poetx_q8& q, Carver& c, ProductI8* p, cudaStream_t st, int dev) {
+  p->w = q.Wq;
+  p->ldw = L.m;
+  if (L.m % 16) {
+    int8_t* w16 = c.take<int8_t>(size_t(L.n) * row16(L.m));
+    POETX_CUDA_ERR(pad_rows(q.Wq, L.n, L.m, w16, st, dev));
+    p->w = w16;
+    p->ldw = row16(L.m);
+  }
+  return cudaSuccess;
+}
+
+// Y = (Xg Diag(G_R)) W~^T with U = Xg Diag(G_R) quantised row by row and the
+// W0 product in int8.
+cudaError_t y_from_xg_i8(const poetx_layer& L, int64_t T, const poetx_q8& q, const void* Xg, void* Y, void* U,
+                         Carver& c, cudaStream_t st, int dev) {
+  const int et = elem_type(L.dtype);
+  PROFILED(ST_BLOCKDIAG, st,
+           POETX_CUDA_ERR(launch_gemm(blockdiag_desc(Xg, et, T, L.m, L.b, L.GR, false, U, et), use_tc(L.dtype), st,
+                                      dev)));
+  int8_t* uq = c.take<int8_t>(size_t(T) * row16(L.m));
+  float* us = c.take<float>(sizeof(float) * size_t(T));
+  POETX_CUDA_ERR(quantize_rows(T, L.m, U, L.dtype, nullptr, uq, row16(L.m), us, st, dev));
+  ProductI8 p{uq, nullptr, us, q.wscale, Y, row16(L.m), 0, static_cast<int>(T), L.n, L.m, false};
+  POETX_CUDA_ERR(weight_rows(L, q, c, &p, st, dev));
+  return product_i8(p, L.dtype, st, dev);
+}
+
+// dU = dY W~^T with the rows of dY * wscale quantised and the product in int8.
+cudaError_t du_from_dy_i8(const poetx_layer& L, int64_t T, const poetx_q8& q, const void* dY, void* dU, Carver& c,
+                          cudaStream_t st, int dev) {
+  int8_t* gq = c.take<int8_t>(size_t(T) * row16(L.n));
+  float* gs = c.take<float>(sizeof(float) * size_t(T));
+  POETX_CUDA_ERR(quantize_rows(T, L.n, dY, L.dtype, q.wscale, gq, row16(L.n), gs, st, dev));
+  ProductI8 p{gq, nullptr, gs, nullptr, dU, row16(L.n), 0, static_cast<int>(T), L.m, L.n, true};
+  POETX_CUDA_ERR(weight_rows(L, q, c, &p, st, dev));
+  return product_i8(p, L.dtype, st, dev);
+}
+
+// One side of the backward from a checkpoint: O_j = D_j G_j^T (O NULL skips
+// it) and the partial sums of dG_j = X_j^T D_j.  `expanded`: [T][d] scratch
+// where expands_checkpoint.
+poetx_status side_q8(const poetx_layer& L, int64_t T, int32_t d, const int8_t* codes, const uint8_t* exps,
+                     const void* D, const void* G, void* O, float* part, int splits, void* expanded, cudaStream_t st,
+                     int dev) {
+  const int et = elem_type(L.dtype);
+  const bool tc_path = use_tc(L.dtype);
+  if (use_pair_bdg8(L.b, L.dtype)) {
+    PROFILED(ST_BDG, st, POETX_CUDA(launch_bdg8(D, codes, exps, G, O, part, T, d, splits, st, dev)));
+  } else if (L.dtype == POETX_FP32) {
+    PROFILED(ST_BDG, st, POETX_CUDA(launch_block_f32(D, codes, exps, G, O, part, T, d, L.b, splits, st)));
+  } else {
+    POETX_CUDA(checkpoint_load(T, d, codes, exps, L.dtype, expanded, st, dev));
+    if (O) PROFILED(ST_BLOCKDIAG, st, POETX_CUDA(launch_gemm(blockdiag_desc(D, et, T, d, L.b, G, true, O, et), tc_path, st, dev)));
+    PROFILED(ST_DG, st, POETX_CUDA(launch_gemm(blockgrad_desc(expanded, D, et, T, d, L.b, splits, part), tc_path, st, dev)));
+  }
+  return POETX_OK;
+}
+
+}  // namespace
+
+// ======================================================================== ABI
+
+extern "C" {
+
+const char* poetx_status_string(int status) {
+  switch (status) {
+    case POETX_OK: return "POETX_OK";
+    case POETX_E_ARG: return "POETX_E_ARG: null pointer, negative size or bad flag";
+    case POETX_E_SHAPE: return "POETX_E_SHAPE: b must divide m and n (and be a multiple of 64 for bf16)";
+    case POETX_E_DTYPE: return "POETX_E_DTYPE: unknown dtype";
+    case POETX_E_ALIGN: return "POETX_E_ALIGN: pointer not 16-byte aligned";
+    case POETX_E_WORKSPACE: return "POETX_E_WORKSPACE: workspace missing or too small";
+    case POETX_E_ARCH: return "POETX_E_ARCH: current device is not compute capability 10.0 (B200)";
+    case POETX_E_CUDA: return "POETX_E_CUDA: CUDA runtime error while queueing work";
+    default: return "POETX: unknown status";
+  }
+}
+
+int32_t poetx_version(void) { return 10100; }
+
+poetx_status poetx_device_error(uint32_t* code) {
+  if (!code) return POETX_E_ARG;
+  int dev;
+  POETX_TRY(current_device(&dev));
+  unsigned int v = 0, zero = 0;
+  POETX_CUDA(cudaDeviceSynchronize());
+  POETX_CUDA(cudaMemcpyFromSymbol(&v, g_device_error, sizeof(v)));
+  POETX_CUDA(cudaMemcpyToSymbol(g_device_error, &zero, sizeof(zero)));
+  *code = v;
+  return POETX_OK;
+}
+
+size_t poetx_cnp_workspace_bytes(int32_t nblk, int32_t b, int32_t dtype) {
+  (void)dtype;
+  if (nblk <= 0 || b < 2) return 0;
+  return kAlign + cnp_bwd_ws(nblk, b);
+}
+
+size_t poetx_layers_cnp_workspace_bytes(int32_t nlayers, const poetx_layer* layers) {
+  if (nlayers < 1 || 2 * nlayers > kMaxSegs || !layers) return 0;
+  int64_t nblk = 0;
+  for (int i = 0; i < nlayers; ++i) {
+    if (check_layer(&layers[i]) != POETX_OK || layers[i].b != layers[0].b || layers[i].dtype != layers[0].dtype)
+      return 0;
+    nblk += layers[i].m / layers[i].b + layers[i].n / layers[i].b;
+  }
+  const int b = layers[0].b;
+  return kAlign + 3 * cnp_units(static_cast<int32_t>(nblk), b) +
+         al(size_t(dtype_size(layers[0].dtype)) * size_t(nblk) * b * b);
+}
+
+poetx_status poetx_layers_cnp_build(int32_t nlayers, const poetx_layer* layers, void* ws, size_t ws_bytes,
+                                    void* stream) {
+  if (nlayers < 1 || 2 * nlayers > kMaxSegs || !layers) return POETX_E_ARG;
+  for (int i = 0; i < nlayers; ++i) {
+    POETX_TRY(check_layer(&layers[i]));
+    if (layers[i].b != layers[0].b) return POETX_E_SHAPE;
+    if (layers[i].dtype != layers[0].dtype) return POETX_E_DTYPE;
+  }
+  if (!ws || ws_bytes < poetx_layers_cnp_workspace_bytes(nlayers, layers)) return POETX_E_WORKSPACE;
+  int dev;
+  POETX_TRY(current_device(&dev));
+  Segs sg{};
+  sg.n = 2 * nlayers;
+  int blk = 0;
+  for (int i = 0; i < nlayers; ++i) {
+    const poetx_layer& L = layers[i];
+    sg.start[2 * i] = blk;
+    sg.q[2 * i] = L.qR;
+    sg.G[2 * i] = L.GR;
+    blk += L.m / L.b;
+    sg.start[2 * i + 1] = blk;
+    sg.q[2 * i + 1] = L.qP;
+    sg.G[2 * i + 1] = L.GP;
+    blk += L.n / L.b;
+  }
+  sg.start[sg.n] = blk;
+  Carver c(ws, ws_bytes);
+  return cnp_build_segs(layers[0].b, layers[0].dtype, sg, c, static_cast<cudaStream_t>(stream), dev);
+}
+
+size_t poetx_layer_cnp_workspace_bytes(const poetx_layer* layer) {
+  if (check_layer(layer) != POETX_OK) return 0;
+  return kAlign + cnp_bwd_ws(layer->m / layer->b + layer->n / layer->b, layer->b);
+}
+
+poetx_status poetx_layer_cnp_build(const poetx_layer* layer, void* ws, size_t ws_bytes, void* stream) {
+  POETX_TRY(check_layer(layer));
+  if (!ws || ws_bytes < poetx_layer_cnp_workspace_bytes(layer)) return POETX_E_WORKSPACE;
+  int dev;
+  POETX_TRY(current_device(&dev));
+  const poetx_layer& L = *layer;
+  Carver c(ws, ws_bytes);
+  return cnp_build2(L.b, L.dtype, L.qR, L.m / L.b, L.GR, L.qP, L.n / L.b, L.GP, c, static_cast<cudaStream_t>(stream),
+                    dev);
+}
+
+size_t poetx_forward_workspace_bytes(const poetx_layer* layer, int64_t T) {
+  if (check_layer(layer) != POETX_OK || T < 0 || T > kMaxT) return 0;
+  return fwd_ws(layer, T);
+}
+
+size_t poetx_backward_workspace_bytes(const poetx_layer* layer, int64_t T) {
+  if (check_layer(layer) != POETX_OK || T < 0 || T > kMaxT) return 0;
+  return bwd_ws(layer, T);
+}
+
+size_t poetx_backward_recompute_workspace_bytes(const poetx_layer* layer, int64_t T) {
+  if (check_layer(layer) != POETX_OK || T < 0 || T > kMaxT) return 0;
+  return bwd_recompute_ws(layer, T);
+}
+
+size_t poetx_merge_workspace_bytes(const poetx_layer* layer) {
+  if (check_layer(layer) != POETX_OK) return 0;
+  return merge_ws(layer);
+}
+
+size_t poetx_check_perm_workspace_bytes(int32_t len) {
+  if (len <= 0) return 0;
+  return kAlign + al(sizeof(int32_t) * size_t(len));
+}
+
+poetx_status poetx_frame_import(const poetx_layer* layer, const void* W0lin, void* stream) {
+  POETX_TRY(check_layer(layer));
+  POETX_TRY(check_ptr(W0lin));
+  int dev;
+  POETX_TRY(current_device(&dev));
+  const poetx_layer& L = *layer;
+  // W[j'][i'] = W0lin[permP[j']][permR[i']]
+  POETX_CUDA(gather_dt(L.dtype, W0lin, L.m, L.n, L.W, L.m, L.n, L.m, L.permR, L.permP,
+                       static_cast<cudaStream_t>(stream), dev));
+  return POETX_OK;
+}
+
+poetx_status poetx_frame_export(const poetx_layer* layer, void* W0lin, void* stream) {
+  POETX_TRY(check_layer(layer));
+  POETX_TRY(check_ptr(W0lin));
+  int dev;
+  POETX_TRY(current_device(&dev));
+  const poetx_layer& L = *layer;
+  // W0lin[permP[j']][permR[i']] = W[j'][i']
+  POETX_CUDA(scatter_dt(L.dtype, L.W, L.m, W0lin, L.m, L.n, L.n, L.m, L.permR, L.permP,
+                        static_cast<cudaStream_t>(stream), dev));
+  return POETX_OK;
+}
+
+poetx_status poetx_cnp_build(int32_t nblk, int32_t b, const float* q, int32_t dtype, void* G, void* ws,
+                             size_t ws_bytes, void* stream) {
+  POETX_TRY(check_dtype_b(dtype, b));
+  if (nblk < 0) return POETX_E_ARG;
+  if (nblk == 0) return POETX_OK;
+  POETX_TRY(check_ptr(q));
+  POETX_TRY(check_ptr(G));
+  if (!ws || ws_bytes < poetx_cnp_workspace_bytes(nblk, b, dtype)) return POETX_E_WORKSPACE;
+  int dev;
+  POETX_TRY(current_device(&dev));
+  Carver c(ws, ws_bytes);
+  return cnp_build2(b, dtype, q, nblk, G, nullptr, 0, nullptr, c, static_cast<cudaStream_t>(stream), dev);
+}
+
+poetx_status poetx_cnp_backward(int32_t nblk, int32_t b, const float* q, const float* dG, float* dq,
+                                int32_t accumulate, int32_t dtype, void* ws, size_t ws_bytes, void* stream) {
+  POETX_TRY(check_dtype_b(dtype, b));
+  if (nblk < 0) return POETX_E_ARG;
+  if (nblk == 0) return POETX_OK;
+  POETX_TRY(check_ptr(q));
+  POETX_TRY(check_ptr(dG));
+  POETX_TRY(check_ptr(dq));
+  if (!ws || ws_bytes < poetx_cnp_workspace_bytes(nblk, b, dtype)) return POETX_E_WORKSPACE;
+  int dev;
+  POETX_TRY(current_device(&dev));
+  Carver c(ws, ws_bytes);
+  return cnp_backward2(b, dtype, q, nblk, dG, 1, dq, nullptr, 0, nullptr, 1, nullptr, accumulate, c,
+                       static_cast<cudaStream_t>(stream), dev);
+}
+
+static poetx_status forward_impl(const poetx_layer* layer, int64_t T, const void* x, void* z, void* y_save,
+                                 void* xg_save, const poetx_q8* q, void* ws, size_t ws_bytes, void* stream) {
+  POETX_TRY(check_layer(layer));
+  if (T < 0) return POETX_E_ARG;
+  if (T > kMaxT) return POETX_E_SHAPE;
+  if (T == 0) return POETX_OK;
+  POETX_TRY(check_ptr(x));
+  POETX_TRY(check_ptr(z));
+  if (y_save && !aligned16(y_save)) return POETX_E_ALIGN;
+  if (xg_save && !aligned16(xg_save)) return POETX_E_ALIGN;
+  if (!ws || ws_bytes < (q ? fwd_q8_ws(layer, T, *q) : fwd_ws(layer, T))) return POETX_E_WORKSPACE;
+  int dev;
+  POETX_TRY(current_device(&dev));
+  const poetx_layer& L = *layer;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int et = elem_type(L.dtype);
+  const size_t es = dtype_size(L.dtype);
+  const bool tc_path = use_tc(L.dtype);
+  if (!q && !y_save && !xg_save && weight_centric_forward(L, T)) {
+    // two [n][m] weights fit in the workspace whenever this path is chosen
+    Carver cw(ws, ws_bytes);
+    if (cw.fits(2 * al(es * size_t(L.n) * L.m))) {
+      void* W1 = cw.take<uint8_t>(es * size_t(L.n) * L.m);
+      void* W2 = cw.take<uint8_t>(es * size_t(L.n) * L.m);
+      // W1 = W~ Diag(G_R)^T, W2 = Diag(G_P)^T W1, W1 = W2 in natural order
+      PROFILED(ST_BLOCKDIAG, st,
+               POETX_CUDA(launch_gemm(blockdiag_desc(L.W, et, L.n, L.m, L.b, L.GR, true, W1, et), tc_path, st, dev)));
+      POETX_CUDA(fold_p_rows(L, W1, W2, st, dev));
+      PROFILED(ST_PERMUTE, st,
+               POETX_CUDA(scatter_dt(L.dtype, W2, L.m, W1, L.m, L.n, L.n, L.m, L.permR, L.permP, st, dev)));
+      // z = x W1^T
+      GemmDesc g;
+      g.M = static_cast<int>(T);
+      g.N = L.n;
+      g.K = L.m;
+      g.A = colblocks_view(x, et, T, L.m, 0);
+      Operand2D b;
+      b.ptr = W1;
+      b.et = et;
+      b.rows = L.n;
+      b.cols = L.m;
+      b.ld = L.m;
+      b.mn_major = false;
+      g.B = b;
+      g.C.ptr = z;
+      g.C.et = et;
+      g.C.ld = L.n;
+      g.C.view_rows = T;
+      g.C.view_cols = L.n;
+      PROFILED(ST_W0, st, POETX_CUDA(launch_gemm(g, tc_path, st, dev)));
+      return POETX_OK;
+    }
+  }
+  Carver c(ws, ws_bytes);
+  void* Xw = c.take<uint8_t>(es * T * L.m);
+  void* Xg = xg_save ? xg_save : Xw;
+  void* U = c.take<uint8_t>(es * T * L.m);
+  void* V = c.take<uint8_t>(es * T * L.n);
+  void* Yw = c.take<uint8_t>(es * T * L.n);
+  void* Y = y_save ? y_save : Yw;
+  // Xg = x Psi_R^T  (columns gathered into the Psi_R frame)
+  PROFILED(ST_PERMUTE, st, POETX_CUDA(permute_dt(L.dtype, x, Xg, T, L.m, L.permR, 0, st, dev)));
+  if (q && q->xg_codes) POETX_CUDA(checkpoint_save(T, L.m, Xg, L.dtype, q->xg_codes, q->xg_exps, st, dev));
+  // Y = (Xg Diag(G_R)) W~^T  (W~ = Psi_R W0 Psi_P^T stored [n][m]); U in `U`, or,
+  // with POETX_FOLD_R and T > n, the weight with G_R folded in
+  if (q && q->Wq) POETX_CUDA(y_from_xg_i8(L, T, *q, Xg, Y, U, c, st, dev));
+  else POETX_CUDA(y_from_xg(L, T, Xg, Y, U, st, dev));
+  if (q && q->y_codes) POETX_CUDA(checkpoint_save(T, L.n, Y, L.dtype, q->y_codes, q->y_exps, st, dev));
+  // V_j = Y_j G_Pj
+  PROFILED(ST_BLOCKDIAG, st, POETX_CUDA(launch_gemm(blockdiag_desc(Y, et, T, L.n, L.b, L.GP, false, V, et), tc_path, st, dev)));
+  // z = V Psi_P  (columns scattered back to natural order)
+  PROFILED(ST_PERMUTE, st, POETX_CUDA(permute_dt(L.dtype, V, z, T, L.n, L.permP, 1, st, dev)));
+  return POETX_OK;
+}
+
+poetx_status poetx_forward(const poetx_layer* layer, int64_t T, const void* x, void* z, void* y_save,
+                           void* xg_save, void* ws, size_t ws_bytes, void* stream) {
+  return forward_impl(layer, T, x, z, y_save, xg_save, nullptr, ws, ws_bytes, stream);
+}
+
+poetx_status poetx_forward_q8(const poetx_layer* layer, int64_t T, const void* x, void* z, void* y_save,
+                              void* xg_save, const poetx_q8* q8, void* ws, size_t ws_bytes, void* stream) {
+  POETX_TRY(check_q8(layer, q8));
+  if ((q8->y_codes && y_save) || (q8->xg_codes && xg_save)) return POETX_E_ARG;
+  return forward_impl(layer, T, x, z, y_save, xg_save, q8, ws, ws_bytes, stream);
+}
+
+size_t poetx_forward_q8_workspace_bytes(const poetx_layer* layer, int64_t T, const poetx_q8* q8) {
+  if (check_q8(layer, q8) != POETX_OK || T < 0 || T > kMaxT) return 0;
+  return fwd_q8_ws(layer, T, *q8);
+}
+
+// Backward of one layer.  Gradient mode "dq" (dGR == dGP == NULL): the
+// packed dq of both sides through the CNP backward.  Mode "dG" (dqR == dqP
+// == NULL): the token sums dG of both sides, CNP backward left to the caller.
+// With `q`, Y and Xg may come from 8-bit checkpoints and the W0 product of
+// the gradient may run in int8.
+static poetx_status backward_impl(const poetx_layer* layer, int64_t T, const void* x, const void* y_save,
+                           const void* xg_save, const poetx_q8* q, const void* dz, void* dx, float* dqR, float* dqP,
+                           float* dGR, float* dGP, int32_t accumulate, void* ws, size_t ws_bytes, void* stream) {
+  POETX_TRY(check_layer(layer));
+  if (T < 0) return POETX_E_ARG;
+  if (T > kMaxT) return POETX_E_SHAPE;
+  const bool dg_mode = dGR != nullptr;
+  const poetx_layer& L = *layer;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int nR = L.m / L.b, nP = L.n / L.b;
+  const size_t outR = dg_mode ? size_t(nR) * L.b * L.b : size_t(nR) * L.b * (L.b - 1) / 2;
+  const size_t outP = dg_mode ? size_t(nP) * L.b * L.b : size_t(nP) * L.b * (L.b - 1) / 2;
+  float* oR = dg_mode ? dGR : dqR;
+  float* oP = dg_mode ? dGP : dqP;
+  if (T == 0) {
+    if (!accumulate) {
+      POETX_CUDA(cudaMemsetAsync(oR, 0, sizeof(float) * outR, st));
+      POETX_CUDA(cudaMemsetAsync(oP, 0, sizeof(float) * outP, st));
+    }
+    return POETX_OK;
+  }
+  const bool y8 = q && q->y_codes, xg8 = q && q->xg_codes, i8 = q && q->Wq;
+  if (!xg_save && !xg8) POETX_TRY(check_ptr(x));
+  if (y_save && !aligned16(y_save)) return POETX_E_ALIGN;
+  POETX_TRY(check_ptr(dz));
+  if (xg_save && !aligned16(xg_save)) return POETX_E_ALIGN;
+  if (dx && !aligned16(dx)) return POETX_E_ALIGN;
+  const bool recompute = y_save == nullptr && !y8;
+  const size_t need = q ? bwd_q8_ws(layer, T, *q, recompute) : recompute ? bwd_recompute_ws(layer, T) : bwd_ws(layer, T);
+  if (!ws || ws_bytes < need) return POETX_E_WORKSPACE;
+  int dev;
+  POETX_TRY(current_device(&dev));
+  const int et = elem_type(L.dtype);
+  const size_t es = dtype_size(L.dtype);
+  const bool tc_path = use_tc(L.dtype);
+  const int64_t mx = L.m > L.n ? L.m : L.n;
+  const size_t bb = size_t(L.b) * L.b;
+  const int sP = y8 ? block_backward_splits(T, L.n, L.b, L.dtype) : dg_splits(nP, L.b, T, L.dtype);
+  const int sR = xg8 ? block_backward_splits(T, L.m, L.b, L.dtype) : dg_splits(nR, L.b, T, L.dtype);
+  Carver c(ws, ws_bytes);
+  void* bufA = c.take<uint8_t>(es * T * mx);
+  void* bufB = c.take<uint8_t>(es * T * mx);
+  void* dU = c.take<uint8_t>(es * T * L.m);
+  float* partP = c.take<float>(sizeof(float) * sP * nP * bb);
+  float* partR = c.take<float>(sizeof(float) * sR * nR * bb);
+  // dG mode: a single split without accumulation goes straight to dG
+  if (dg_mode && !accumulate && sP == 1) partP = dGP;
+  if (dg_mode && !accumulate && sR == 1) partR = dGR;
+
+  if (recompute) {
+    // "mem" variant: Y was not kept; recompute it from x (Xg, then Y as in the forward)
+    void* Ybuf = c.take<uint8_t>(es * T * L.n);
+    void* Xbuf = c.take<uint8_t>(es * T * L.m);
+    const void* xg = xg_save;
+    if (xg8) {
+      // from the checkpoint: Y is then that of the checkpoint's values
+      POETX_CUDA(checkpoint_load(T, L.m, q->xg_codes, q->xg_exps, L.dtype, Xbuf, st, dev));
+      xg = Xbuf;
+    } else if (!xg_save) {
+      PROFILED(ST_PERMUTE, st, POETX_CUDA(permute_dt(L.dtype, x, Xbuf, T, L.m, L.permR, 0, st, dev)));
+      xg_save = xg = Xbuf;
+    }
+    // the forward's Y, by the same arithmetic (dU, written only later, holds U or the folded weight)
+    if (i8) {
+      Carver scratch = c;  // its int8 rows are done before the gradient's take their place
+      POETX_CUDA(y_from_xg_i8(L, T, *q, xg, Ybuf, dU, scratch, st, dev));
+    } else {
+      POETX_CUDA(y_from_xg(L, T, xg, Ybuf, dU, st, dev));
+    }
+    y_save = Ybuf;
+  }
+  // Y or Xg expanded, where the products do not read the checkpoint itself
+  void* expanded = (y8 || xg8) && expands_checkpoint(L) ? c.take<uint8_t>(es * T * mx) : nullptr;
+
+  // dV = dz Psi_P^T
+  void* dV = bufA;
+  PROFILED(ST_PERMUTE, st, POETX_CUDA(permute_dt(L.dtype, dz, dV, T, L.n, L.permP, 0, st, dev)));
+  // dY_j = dV_j G_Pj^T and dG_Pj = Y_j^T dV_j (split over tokens): one kernel
+  // reading dV once (b = 256 bf16), else two GEMMs.  With POETX_FOLD_P and
+  // T > m (bf16) dY is not formed at all: G_P is folded into the weight (W_P = Diag(G_P)^T W~,
+  // [n][m], one weight-sized pass) and dU = dV W_P below, so only the dG
+  // product reads dV here.
+  void* dY = bufB;
+  const bool fold_p = fold_p_into_weight(L, T);
+  if (y8) {
+    POETX_TRY(side_q8(L, T, L.n, q->y_codes, q->y_exps, dV, L.GP, dY, partP, sP, expanded, st, dev));
+  } else if (fold_p) {
+    POETX_CUDA(fold_p_rows(L, L.W, bufB, st, dev));
+    PROFILED(ST_DG, st, POETX_CUDA(launch_gemm(blockgrad_desc(y_save, dV, et, T, L.n, L.b, sP, partP), tc_path, st, dev)));
+  } else if (use_pair_bdg(L)) {
+    PROFILED(ST_BDG, st, POETX_CUDA(launch_bdg(dV, y_save, L.GP, dY, partP, T, L.n, sP, st, dev)));
+  } else {
+    PROFILED(ST_BLOCKDIAG, st, POETX_CUDA(launch_gemm(blockdiag_desc(dV, et, T, L.n, L.b, L.GP, true, dY, et), tc_path, st, dev)));
+    PROFILED(ST_DG, st, POETX_CUDA(launch_gemm(blockgrad_desc(y_save, dV, et, T, L.n, L.b, sP, partP), tc_path, st, dev)));
+  }
+  // dU = dY W~^T  (B(k=j', n=i') = W[j'][i'], MN-major), or dU = dV W_P
+  if (i8) {
+    Carver scratch = c;
+    POETX_CUDA(du_from_dy_i8(L, T, *q, dY, dU, scratch, st, dev));
+  } else {
+    GemmDesc g;
+    g.M = static_cast<int>(T);
+    g.N = L.m;
+    g.K = L.n;
+    g.A = colblocks_view(fold_p ? dV : dY, et, T, L.n, 0);
+    Operand2D b;
+    b.ptr = fold_p ? bufB : L.W;
+    b.et = et;
+    b.rows = L.n;
+    b.cols = L.m;
+    b.ld = L.m;
+    b.mn_major = true;
+    g.B = b;
+    g.C.ptr = dU;
+    g.C.et = et;
+    g.C.ld = L.m;
+    g.C.view_rows = T;
+    g.C.view_cols = L.m;
+    PROFILED(ST_W0, st, POETX_CUDA(launch_gemm(g, tc_path, st, dev)));
+  }
+  // Xg = x Psi_R^T: the forward's copy when it saved one, else re-gathered (dV is dead)
+  const void* Xg = xg_save;
+  if (!Xg && !xg8) {
+    Xg = bufA;
+    PROFILED(ST_PERMUTE, st, POETX_CUDA(permute_dt(L.dtype, x, bufA, T, L.m, L.permR, 0, st, dev)));
+  }
+  // dXg_j = dU_j G_Rj^T (dY is dead; only with dx) and dG_Rj = Xg_j^T dU_j
+  void* dXg = bufB;
+  if (xg8) {
+    POETX_TRY(side_q8(L, T, L.m, q->xg_codes, q->xg_exps, dU, L.GR, dx ? dXg : nullptr, partR, sR, expanded, st, dev));
+  } else if (use_pair_bdg(L)) {
+    PROFILED(ST_BDG, st, POETX_CUDA(launch_bdg(dU, Xg, L.GR, dx ? dXg : nullptr, partR, T, L.m, sR, st, dev)));
+  } else {
+    if (dx) PROFILED(ST_BLOCKDIAG, st, POETX_CUDA(launch_gemm(blockdiag_desc(dU, et, T, L.m, L.b, L.GR, true, dXg, et), tc_path, st, dev)));
+    PROFILED(ST_DG, st, POETX_CUDA(launch_gemm(blockgrad_desc(Xg, dU, et, T, L.m, L.b, sR, partR), tc_path, st, dev)));
+  }
+  // dx = dXg Psi_R
+  if (dx) PROFILED(ST_PERMUTE, st, POETX_CUDA(permute_dt(L.dtype, dXg, dx, T, L.m, L.permR, 1, st, dev)));
+  if (dg_mode) {
+    // dG = fixed-order sum of the token splits (skipped when the GEMM wrote dG)
+    const bool sumP = partP != dGP, sumR = partR != dGR;
+    const int64_t elP = int64_t(nP) * int64_t(bb), elR = int64_t(nR) * int64_t(bb);
+    if ((sumP || sumR) && (elP % 4 || elR % 4)) {  // blocks of odd size: sums that are no whole vectors
+      if (sumP)
+        PROFILED(ST_REDUCE, st, q8::add_splits_kernel<<<grid_for(elP, 256, dev), 256, 0, st>>>(partP, sP, elP, dGP, accumulate));
+      if (sumR)
+        PROFILED(ST_REDUCE, st, q8::add_splits_kernel<<<grid_for(elR, 256, dev), 256, 0, st>>>(partR, sR, elR, dGR, accumulate));
+      POETX_CUDA(cudaGetLastError());
+    } else if (sumP || sumR) {
+      const int64_t n4P = sumP ? int64_t(nP) * int64_t(bb) / 4 : 0;
+      const int64_t n4R = sumR ? int64_t(nR) * int64_t(bb) / 4 : 0;
+      PROFILED(ST_REDUCE, st,
+               sum_splits2_kernel<<<grid_for(n4P + n4R, 256, dev), 256, 0, st>>>(
+                   reinterpret_cast<const float4*>(partP), sP, n4P, reinterpret_cast<float4*>(dGP),
+                   reinterpret_cast<const float4*>(partR), sR, n4R, reinterpret_cast<float4*>(dGR), accumulate));
+      POETX_CUDA(cudaGetLastError());
+    }
+    return POETX_OK;
+  }
+  // dq from the dG partial sums of both sides (fixed-order reduction of the
+  // token splits inside the CNP backward)
+  POETX_TRY(cnp_backward2(L.b, L.dtype, L.qP, nP, partP, sP, dqP, L.qR, nR, partR, sR, dqR, accumulate, c, st, dev));
+  return POETX_OK;
+}
+
+poetx_status poetx_backward(const poetx_layer* layer, int64_t T, const void* x, const void* y_save,
+                            const void* xg_save, const void* dz, void* dx, float* dqR, float* dqP,
+                            int32_t accumulate, void* ws, size_t ws_bytes, void* stream) {
+  POETX_TRY(check_ptr(dqR));
+  POETX_TRY(check_ptr(dqP));
+  return backward_impl(layer, T, x, y_save, xg_save, nullptr, dz, dx, dqR, dqP, nullptr, nullptr, accumulate, ws,
+                       ws_bytes, stream);
+}
+
+size_t poetx_backward_q8_workspace_bytes(const poetx_layer* layer, int64_t T, int32_t have_y, const poetx_q8* q8) {
+  if (check_q8(layer, q8) != POETX_OK || T < 0 || T > kMaxT) return 0;
+  return bwd_q8_ws(layer, T, *q8, !have_y && !q8->y_codes);
+}
+
+poetx_status poetx_backward_q8(const poetx_layer* layer, int64_t T, const void* x, const void* y_save,
+                               const void* xg_save, const poetx_q8* q8, const void* dz, void* dx, float* dqR,
+                               float* dqP, int32_t accumulate, void* ws, size_t ws_bytes, void* stream) {
+  POETX_TRY(check_q8(layer, q8));
+  if ((q8->y_codes && y_save) || (q8->xg_codes && xg_save)) return POETX_E_ARG;
+  POETX_TRY(check_ptr(dqR));
+  POETX_TRY(check_ptr(dqP));
+  return backward_impl(layer, T, x, y_save, xg_save, q8, dz, dx, dqR, dqP, nullptr, nullptr, accumulate, ws, ws_bytes,
+                       stream);
+}
+
+poetx_status poetx_backward_dG_q8(const poetx_layer* layer, int64_t T, const void* x, const void* y_save,
+                                  const void* xg_save, const poetx_q8* q8, const void* dz, void* dx, float* dGR,
+                                  float* dGP, int32_t accumulate, void* ws, size_t ws_bytes, void* stream) {
+  POETX_TRY(check_q8(layer, q8));
+  if ((q8->y_codes && y_save) || (q8->xg_codes && xg_save)) return POETX_E_ARG;
+  POETX_TRY(check_ptr(dGR));
+  POETX_TRY(check_ptr(dGP));
+  return backward_impl(layer, T, x, y_save, xg_save, q8, dz, dx, nullptr, nullptr, dGR, dGP, accumulate, ws, ws_bytes,
+                       stream);
+}
+
+poetx_status poetx_backward_dG(const poetx_layer* layer, int64_t T, const void* x, const void* y_save,
+                               const void* xg_save, const void* dz, void* dx, float* dGR, float* dGP,
+                               int32_t accumulate, void* ws, size_t ws_bytes, void* stream) {
+  POETX_TRY(check_ptr(dGR));
+  POETX_TRY(check_ptr(dGP));
+  return backward_impl(layer, T, x, y_save, xg_save, nullptr, dz, dx, nullptr, nullptr, dGR, dGP, accumulate, ws,
+                       ws_bytes, stream);
+}
+
+poetx_status poetx_merge(const poetx_layer* layer, const int32_t* new_permR, const int32_t* new_permP,
+                         void* W_out, void* ws, size_t ws_bytes, void* stream) {
+  POETX_TRY(check_layer(layer));
+  POETX_TRY(check_ptr(new_permR));
+  POETX_TRY(check_ptr(new_permP));
+  POETX_TRY(check_ptr(W_out));
+  const poetx_layer& L = *layer;
+  const size_t es = dtype_size(L.dtype);
+  const size_t wbytes = es * size_t(L.n) * L.m;
+  {
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(L.W), b0 = reinterpret_cast<uintptr_t>(W_out);
+    if (a0 < b0 + wbytes && b0 < a0 + wbytes) return POETX_E_ARG;
+  }
+  if (!ws || ws_bytes < merge_ws(layer)) return POETX_E_WORKSPACE;
+  int dev;
+  POETX_TRY(current_device(&dev));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int et = elem_type(L.dtype);
+  const bool tc_path = use_tc(L.dtype);
+  const int nR = L.m / L.b, nP = L.n / L.b;
+  const size_t nm = size_t(L.n) * L.m;
+  Carver c(ws, ws_bytes);
+  float* B1t = c.take<float>(sizeof(float) * nm);
+  float* At = c.take<float>(sizeof(float) * nm);
+  float* GPt = c.take<float>(sizeof(float) * size_t(nP) * L.b * L.b);
+  int32_t* invR = c.take<int32_t>(sizeof(int32_t) * L.m);
+  int32_t* invP = c.take<int32_t>(sizeof(int32_t) * L.n);
+  int32_t* sigR = c.take<int32_t>(sizeof(int32_t) * L.m);
+  int32_t* sigP = c.take<int32_t>(sizeof(int32_t) * L.n);
+
+  // Stored W~ = (Psi_R W0 Psi_P^T)^T.  New weight R W0 P in the old frame is
+  // A' = Diag(G_R) W~ Diag(G_P), stored transposed:
+  //   At = Diag(G_P)^T . W . Diag(G_R)^T     ([n][m])
+  // pass 1: B1t = Diag(G_R) . W^T ([m][n]); block i: B1t[ib + r][c] = sum_k G_Ri[r][k] W[c][ib + k]
+  {
+    GemmDesc g;
+    g.M = L.b;
+    g.N = L.n;
+    g.K = L.b;
+    g.batch = nR;
+    g.A = blocks_view(L.GR, et, nR, L.b, true);          // A(r, k) = G_Ri[r][k]
+    g.B = colblocks_view(L.W, et, L.n, L.m, L.b);        // B(k, c) = W[c][ib + k]
+    g.C.ptr = B1t;
+    g.C.et = ET_F32;
+    g.C.ld = L.n;
+    g.C.batch_stride = int64_t(L.b) * L.n;
+    g.C.view_rows = L.m;
+    g.C.view_cols = L.n;
+    g.C.b_row = L.b;
+    PROFILED(ST_MERGE, st, POETX_CUDA(launch_gemm(g, tc_path, st, dev)));
+  }
+  // pass 2: At[jb + r][c] = sum_k G_Pj[k][r] B1t[c][jb + k]  (G_Pj^T, fp32, K-major)
+  {
+    const dim3 tgrid((L.b + 31) / 32, (L.b + 31) / 32, nP), tblock(32, 8);
+    if (L.dtype == POETX_BF16)
+      PROFILED(ST_MERGE, st, transpose_blocks_kernel<<<tgrid, tblock, 0, st>>>(
+                                 static_cast<const __nv_bfloat16*>(L.GP), GPt, L.b));
+    else
+      PROFILED(ST_MERGE, st,
+               transpose_blocks_kernel<<<tgrid, tblock, 0, st>>>(static_cast<const float*>(L.GP), GPt, L.b));
+    POETX_CUDA(cudaGetLastError());
+    GemmDesc g;
+    g.M = L.b;
+    g.N = L.m;
+    g.K = L.b;
+    g.batch = nP;
+    g.A = blocks_view(GPt, ET_F32, nP, L.b, true);       // A(r, k) = G_Pj[k][r]
+    g.B = colblocks_view(B1t, ET_F32, L.m, L.n, L.b);    // B(k, c) = B1t[c][jb + k]
+    g.C.ptr = At;
+    g.C.et = ET_F32;
+    g.C.ld = L.m;
+    g.C.batch_stride = int64_t(L.b) * L.m;
+    g.C.view_rows = L.n;
+    g.C.view_cols = L.m;
+    g.C.b_row = L.b;
+    PROFILED(ST_MERGE, st, POETX_CUDA(launch_gemm(g, tc_path, st, dev)));
+  }
+  // New frame: W'[j'][i'] = At[sigP[j']][sigR[i']], sig = perm_old^-1 o perm_new.
+  invert_perm_kernel<<<(L.m + 255) / 256, 256, 0, st>>>(L.permR, invR, L.m);
+  invert_perm_kernel<<<(L.n + 255) / 256, 256, 0, st>>>(L.permP, invP, L.n);
+  compose_perm_kernel<<<(L.m + 255) / 256, 256, 0, st>>>(invR, new_permR, sigR, L.m);
+  compose_perm_kernel<<<(L.n + 255) / 256, 256, 0, st>>>(invP, new_permP, sigP, L.n);
+  POETX_CUDA(cudaGetLastError());
+  if (L.dtype == POETX_BF16)
+    POETX_CUDA(gather(static_cast<const float*>(At), L.m, L.n, static_cast<__nv_bfloat16*>(W_out), L.m, L.n, L.m,
+                      sigR, sigP, st, dev));
+  else
+    POETX_CUDA(gather(static_cast<const float*>(At), L.m, L.n, static_cast<float*>(W_out), L.m, L.n, L.m, sigR, sigP,
+                      st, dev));
+  // Reset: Q = 0, G = I.
+  POETX_CUDA(cudaMemsetAsync(L.qR, 0, sizeof(float) * size_t(nR) * L.b * (L.b - 1) / 2, st));
+  POETX_CUDA(cudaMemsetAsync(L.qP, 0, sizeof(float) * size_t(nP) * L.b * (L.b - 1) / 2, st));
+  const int64_t cR = int64_t(nR) * L.b * L.b, cP = int64_t(nP) * L.b * L.b;
+  if (L.dtype == POETX_BF16) {
+    identity_blocks_kernel<__nv_bfloat16>
+        <<<grid_for(cR, 256, dev), 256, 0, st>>>(static_cast<__nv_bfloat16*>(L.GR), nR, L.b);
+    identity_blocks_kernel<__nv_bfloat16>
+        <<<grid_for(cP, 256, dev), 256, 0, st>>>(static_cast<__nv_bfloat16*>(L.GP), nP, L.b);
+  } else {
+    identity_blocks_kernel<float><<<grid_for(cR, 256, dev), 256, 0, st>>>(static_cast<float*>(L.GR), nR, L.b);
+    identity_blocks_kernel<float><<<grid_for(cP, 256, dev), 256, 0, st>>>(static_cast<float*>(L.GP), nP, L.b);
+  }
+  POETX_CUDA(cudaGetLastError());
+  return POETX_OK;
+}
+
+poetx_status poetx_check_perm(const int32_t* perm, int32_t len, int32_t* d_ok, void* ws, size_t ws_bytes,
+                              void* stream) {
+  if (len <= 0) return POETX_E_ARG;
+  POETX_TRY(check_ptr(perm));
+  if (!d_ok) return POETX_E_ARG;
+  if (!ws || ws_bytes < poetx_check_perm_workspace_bytes(len)) return POETX_E_WORKSPACE;
+  int dev;
+  POETX_TRY(current_device(&dev));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Carver c(ws, ws_bytes);
+  int32_t* hist = c.take<int32_t>(sizeof(int32_t) * len);
+  POETX_CUDA(cudaMemsetAsync(hist, 0, sizeof(int32_t) * len, st));
+  set_int_kernel<<<1, 1, 0, st>>>(d_ok, 1);
+  perm_histogram_kernel<<<(len + 255) / 256, 256, 0, st>>>(perm, hist, len, d_ok);
+  perm_check_kernel<<<(len + 255) / 256, 256, 0, st>>>(hist, len, d_ok);
+  POETX_CUDA(cudaGetLastError());
+  return POETX_OK;
+}
+
+int32_t poetx_profile_stage_count(void) { return ST_COUNT; }
+
+const char* poetx_profile_stage_name(int32_t stage) {
+  if (stage < 0 || stage >= ST_COUNT) return "unknown";
+  return kStageNames[stage];
+}
+
+poetx_status poetx_profile_begin(void) {
+  Profiler& P = profiler();
+  std::lock_guard<std::mutex> g(P.mu);
+  P.on = true;
+  P.used = 0;
+  P.recs.clear();
+  P.done.clear();
+  return POETX_OK;
+}
+
+poetx_status poetx_profile_end(double* ms_per_stage, int64_t* launches_per_stage, int32_t nstages) {
+  if (!ms_per_stage || !launches_per_stage || nstages < 0) return POETX_E_ARG;
+  Profiler& P = profiler();
+  std::lock_guard<std::mutex> g(P.mu);
+  for (int i = 0; i < nstages; ++i) {
+    ms_per_stage[i] = 0.0;
+    launches_per_stage[i] = 0;
+  }
+  poetx_status st = POETX_OK;
+  for (const auto& r : P.recs) {
+    if (cudaEventSynchronize(P.pool[r.second + 1]) != cudaSuccess) {
+      (void)cudaGetLastError();
+      st = POETX_E_CUDA;
+      break;
+    }
+    float ms = 0.f;
+    if (cudaEventElapsedTime(&ms, P.pool[r.second], P.pool[r.second + 1]) != cudaSuccess) {
+      (void)cudaGetLastError();
+      st = POETX_E_CUDA;
+      break;
+    }
+    if (r.first < nstages) {
+      ms_per_stage[r.first] += ms;
+      launches_per_stage[r.first] += 1;
+    }
+    P.done.emplace_back(r.first, ms);
+  }
+  P.on = false;
+  P.used = 0;
+  P.recs.clear();
+  return st;
+}
+
+int32_t poetx_profile_records(int32_t* stages, float* ms, int32_t max_records) {
+  Profiler& P = profiler();
+  std::lock_guard<std::mutex> g(P.mu);
+  const int32_t n = static_cast<int32_t>(P.done.size());
+  if (!stages || !ms || max_records <= 0) return n;
+  const int32_t k = n < max_records ? n : max_records;
+  for (int32_t i = 0; i < k; ++i) {
+    stages[i] = P.done[i].first;
+    ms[i] = P.done[i].second;
+  }
+  return n;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- fixed-scratch CNP build
+// Some callers cannot allocate device memory when they build G: a host
+// program that links only this C library and has no device allocator of its
+// own, or a serving process that reserves its whole memory budget at start-up
+// and forbids allocations afterwards.  For them poetx_cnp_build_fixed takes
+// its scratch (Q, S and H for every block) from this file-scope device array
+// instead of a caller workspace.  The array is kFixedScratchBytes on every
+// GPU that loads the library, for the life of the process: b = 256 bf16
+// builds of up to 47 blocks (the pair kernel takes 128 KiB per block plus
+// three per pair of SMs), other builds of up to ~2.09e6 fp32 elements of Q
+// (b = 512: 7 blocks).  Host code must
+// not hand the symbol itself to a kernel (on the host it only names the
+// array); the device address comes from cudaGetSymbolAddress, looked up once
+// per device on that device's first call.
+constexpr size_t kFixedScratchBytes = size_t(24) << 20;
+static __device__ __align__(256) unsigned char g_cnp_fixed_scratch[kFixedScratchBytes];
+
+namespace {
+std::mutex g_fixed_mu;
+void* g_fixed_scratch_ptr[64] = {nullptr};
+
+// Device address of the fixed scratch on the current device `dev`.
+poetx_status fixed_scratch(int dev, void** out) {
+  std::lock_guard<std::mutex> g(g_fixed_mu);
+  if (!g_fixed_scratch_ptr[dev]) {
+    void* p = nullptr;
+    if (cudaGetSymbolAddress(&p, g_cnp_fixed_scratch) != cudaSuccess || !p) {
+      (void)cudaGetLastError();
+      return POETX_E_CUDA;
+    }
+    g_fixed_scratch_ptr[dev] = p;
+  }
+  *out = g_fixed_scratch_ptr[dev];
+  return POETX_OK;
+}
+}  // namespace
+
+extern "C" poetx_status poetx_cnp_build_fixed(int32_t nblk, int32_t b, const float* q, int32_t dtype, void* G,
+                                              void* stream) {
+  POETX_TRY(check_dtype_b(dtype, b));
+  if (nblk < 0) return POETX_E_ARG;
+  if (nblk == 0) return POETX_OK;
+  POETX_TRY(check_ptr(q));
+  POETX_TRY(check_ptr(G));
+  int dev;
+  POETX_TRY(current_device(&dev));
+  // the scratch the build will carve: the fused pair kernel's bf16 operand
+  // region (b = 256 bf16), else Q, S and H in fp32 for every block; requests
+  // that do not fit are refused before anything is queued
+  const size_t need = kAlign + (use_pair_cnp(b, dtype) ? cnp_pair_bytes(nblk, false, false, dev)
+                                                       : 3 * cnp_units(nblk, b));
+  if (need > kFixedScratchBytes) return POETX_E_WORKSPACE;  // too many blocks for the fixed scratch
+  void* scratch = nullptr;
+  POETX_TRY(fixed_scratch(dev, &scratch));
+  // Every scratch matrix (Q, S, H, or the pair kernel's bf16 operands) is
+  // written in full before it is read: nothing to clear.
+  Carver c(scratch, kFixedScratchBytes);
+  return cnp_build2(b, dtype, q, nblk, G, nullptr, 0, nullptr, c, static_cast<cudaStream_t>(stream), dev);
+}
+
+// ---------------------------------------------------------------- failure-path self-test
+// One warp waits on an mbarrier that no thread ever arrives on, through the
+// same bounded wait the GEMM and copy kernels use, with a short limit: the
+// wait gives up, records DERR_GEMM_WAIT in the sticky error word and the
+// kernel returns normally.  No copy, MMA or TMEM allocation is involved, so
+// nothing is left in flight.  out[0] = 1 if the wait ended by an arrival
+// (never expected), out[1] = nanoseconds waited.
+namespace {
+__global__ void stalled_wait_kernel(uint64_t limit_ns, unsigned long long* out) {
+  __shared__ __align__(8) uint64_t bar;
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&bar), 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const uint64_t t0 = global_ns();
+    const bool arrived = mbar_wait_for(smem_u32(&bar), 0, DERR_GEMM_WAIT, limit_ns);
+    out[0] = arrived ? 1ull : 0ull;
+    out[1] = global_ns() - t0;
+  }
+}
+}  // namespace
+
+extern "C" poetx_status poetx_selftest_wait_timeout(uint32_t limit_us, unsigned long long* d_out, void* stream) {
+  if (limit_us < 1 || limit_us > 1000000) return POETX_E_ARG;
+  if (!d_out) return POETX_E_ARG;
+  if (reinterpret_cast<uintptr_t>(d_out) & 7u) return POETX_E_ALIGN;
+  int dev;
+  POETX_TRY(current_device(&dev));
+  stalled_wait_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(uint64_t(limit_us) * 1000ull, d_out);
+  POETX_CUDA(cudaGetLastError());
+  return POETX_OK;
+}
+
+// ---------------------------------------------------------------- POET-XQ weight storage
+extern "C" poetx_status poetx_weight_quantize(int32_t n, int32_t m, const void* W, int32_t dtype, int8_t* Wq,
+                                              float* scale, void* stream) {
+  if (dtype != POETX_FP32 && dtype != POETX_BF16) return POETX_E_DTYPE;
+  if (n < 0 || m <= 0) return POETX_E_ARG;
+  if (n == 0) return POETX_OK;
+  POETX_TRY(check_ptr(W));
+  POETX_TRY(check_ptr(Wq));
+  POETX_TRY(check_ptr(scale));
+  int dev;
+  POETX_TRY(current_device(&dev));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int grid = n < sm_count(dev) * 8 ? n : sm_count(dev) * 8;
+  if (dtype == POETX_BF16)
+    quantize_rows_kernel<<<grid, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(W), n, m, Wq, scale);
+  else
+    quantize_rows_kernel<<<grid, 256, 0, st>>>(static_cast<const float*>(W), n, m, Wq, scale);
+  POETX_CUDA(cudaGetLastError());
+  return POETX_OK;
+}
+
+extern "C" poetx_status poetx_weight_dequantize(int32_t n, int32_t m, const int8_t* Wq, const float* scale,
+                                                int32_t dtype, void* W, void* stream) {
+  if (dtype != POETX_FP32 && dtype != POETX_BF16) return POETX_E_DTYPE;
+  if (n < 0 || m <= 0) return POETX_E_ARG;
+  if (n == 0) return POETX_OK;
+  POETX_TRY(check_ptr(W));
+  POETX_TRY(check_ptr(Wq));
+  POETX_TRY(check_ptr(scale));
+  int dev;
+  POETX_TRY(current_device(&dev));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  PROFILED(ST_DEQUANT, st,
+           POETX_CUDA(dtype == POETX_BF16 ? launch_expand<__nv_bfloat16>(Wq, nullptr, scale, n, m, W, st, dev)
+                                          : launch_expand<float>(Wq, nullptr, scale, n, m, W, st, dev)));
+  return POETX_OK;
+}
+
+// ---------------------------------------------------------------- optimizer step on packed q
+extern "C" poetx_status poetx_adamw_step(int64_t n, float* q, const float* grad, float* m1, float* m2, float lr,
+                                         float beta1, float beta2, float eps, float weight_decay, int32_t step,
+                                         void* stream) {
+  if (n < 0 || step < 1) return POETX_E_ARG;
+  if (n == 0) return POETX_OK;
+  POETX_TRY(check_ptr(q));
+  POETX_TRY(check_ptr(grad));
+  POETX_TRY(check_ptr(m1));
+  POETX_TRY(check_ptr(m2));
+  int dev;
+  POETX_TRY(current_device(&dev));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const float bc1 = static_cast<float>(1.0 - std::pow(static_cast<double>(beta1), step));
+  const float bc2 = static_cast<float>(1.0 - std::pow(static_cast<double>(beta2), step));
+  PROFILED(ST_OPTIM, st,
+           adamw_kernel<<<grid_for((n + 3) / 4, 256, dev), 256, 0, st>>>(n, q, grad, m1, m2, lr, beta1, beta2, eps,
+                                                                         weight_decay, bc1, bc2));
+  POETX_CUDA(cudaGetLastError());
+  return POETX_OK;
+}
+
+// ---------------------------------------------------------------- 8-bit path
 extern "C" {
 
 poetx_status poetx_quantize_rows(int64_t T, int32_t d, const void* x, int32_t dtype, const float* colscale,
@@ -2483,23 +2662,16 @@ poetx_status poetx_block_backward(int64_t T, int32_t d, int32_t b, const int8_t*
   if (!ws || ws_bytes < block_backward_ws(T, d, b, dtype)) return POETX_E_WORKSPACE;
   int dev;
   POETX_TRY(current_device(&dev));
-  const int et = elem_type(dtype);
-  const bool tc_path = use_tc(dtype);
   const int splits = block_backward_splits(T, d, b, dtype);
   const size_t elems = size_t(d) * b;
   Carver c(ws, ws_bytes);
   float* part = c.take<float>(sizeof(float) * splits * elems);
   if (splits == 1 && !accumulate) part = dG;
-  if (use_pair_bdg8(b, dtype)) {
-    PROFILED(ST_BDG, st, POETX_CUDA(launch_bdg8(D, codes, exps, G, O, part, T, d, splits, st, dev)));
-  } else if (dtype == POETX_FP32) {
-    PROFILED(ST_BDG, st, POETX_CUDA(launch_block_f32(D, codes, exps, G, O, part, T, d, b, splits, st)));
-  } else {
-    void* X = c.take<uint8_t>(size_t(dtype_size(dtype)) * T * d);
-    POETX_CUDA(checkpoint_load(T, d, codes, exps, dtype, X, st, dev));
-    if (O) PROFILED(ST_BLOCKDIAG, st, POETX_CUDA(launch_gemm(blockdiag_desc(D, et, T, d, b, G, true, O, et), tc_path, st, dev)));
-    PROFILED(ST_DG, st, POETX_CUDA(launch_gemm(blockgrad_desc(X, D, et, T, d, b, splits, part), tc_path, st, dev)));
-  }
+  poetx_layer L{};
+  L.b = b;
+  L.dtype = dtype;
+  void* X = expands_checkpoint(L) ? c.take<uint8_t>(size_t(dtype_size(dtype)) * T * d) : nullptr;
+  POETX_TRY(side_q8(L, T, d, codes, exps, D, G, O, part, splits, X, st, dev));
   if (part != dG) {
     PROFILED(ST_REDUCE, st,
              q8::add_splits_kernel<<<grid_for(static_cast<int64_t>(elems + 3) / 4, 256, dev), 256, 0, st>>>(

@@ -8,7 +8,7 @@ triangles qR, qP (the trainable parameters) and the G blocks built from them.
 """
 from __future__ import annotations
 
-from typing import NamedTuple, Optional, Tuple
+from typing import NamedTuple, Optional, Tuple, Union
 
 import torch
 
@@ -18,7 +18,9 @@ from . import (POETX_BF16, POETX_FOLD_ALL, POETX_FP32, make_layer, poetx_backwar
                poetx_forward, poetx_forward_workspace_bytes, poetx_frame_export, poetx_frame_import,
                poetx_layer_cnp_build, poetx_layer_cnp_workspace_bytes, poetx_layers_cnp_build,
                poetx_layers_cnp_workspace_bytes, poetx_merge, poetx_merge_workspace_bytes, poetx_weight_dequantize,
-               poetx_weight_quantize, poetx_adamw_step)
+               poetx_weight_quantize, poetx_adamw_step, make_q8, poetx_forward_q8, poetx_forward_q8_workspace_bytes,
+               poetx_backward_q8, poetx_backward_dG_q8, poetx_backward_q8_workspace_bytes)
+from .quantized import Checkpoint, matmul_int8, matmul_int8_grad, quantize_rows
 
 _TORCH_DTYPE = {POETX_BF16: torch.bfloat16, POETX_FP32: torch.float32}
 
@@ -41,9 +43,10 @@ def _need(t, shape, dtype, device: torch.device, name: str) -> None:
 
 class Saved(NamedTuple):
     """Activations the forward keeps for the backward: Y ([T][n], the P-side
-    input in the Psi_P frame) and optionally Xg ([T][m], x in the Psi_R frame)."""
-    y: Optional[torch.Tensor]
-    xg: Optional[torch.Tensor]
+    input in the Psi_P frame) and optionally Xg ([T][m], x in the Psi_R frame),
+    as tensors of the layer dtype or as 8-bit checkpoints (forward(save8=True))."""
+    y: Union[torch.Tensor, Checkpoint, None]
+    xg: Union[torch.Tensor, Checkpoint, None]
 
 
 class PoetxLinear:
@@ -74,16 +77,29 @@ class PoetxLinear:
         self.Wq = None      # POET-XQ: int8 codes of W and per-row scales
         self.Wscale = None
         self._wscratch = None
+        self.int8_product = False
 
     # -------------------------------------------------------------- POET-XQ
-    def quantize_weight(self, scratch: Optional[torch.Tensor] = None, stream=None) -> None:
+    def quantize_weight(self, scratch: Optional[torch.Tensor] = None, stream=None, int8_product: bool = False) -> None:
         """Keep W as int8 codes + per-row scales (POET-XQ) and drop the bf16
         copy; every forward / backward dequantizes it into `scratch` (a flat
         tensor of at least n*m elements of the layer dtype, which several
-        layers may share) right before use."""
+        layers may share) right before use.  With `int8_product` there is no
+        scratch: the W0 product of the forward and of the backward multiplies
+        the codes themselves with its other operand quantized row by row (see
+        poetx_q8 in include/poetx.h); merge and export need the weight and
+        refuse then."""
+        if int8_product and self.fold:
+            raise ValueError("int8_product: the layer folds its blocks into the weight (fold != 0)")
+        if int8_product and scratch is not None:
+            raise ValueError("scratch: not used with int8_product")
         self.Wq = torch.empty((self.n, self.m), dtype=torch.int8, device=self.device)
         self.Wscale = torch.empty(self.n, dtype=torch.float32, device=self.device)
         poetx_weight_quantize(self.n, self.m, self.W, self.dtype, self.Wq, self.Wscale, stream)
+        self.int8_product = int8_product
+        if int8_product:
+            self.W = self.Wq  # (stands for the pointer only: no call of this mode reads it)
+            return
         if scratch is None:
             scratch = torch.empty(self.n * self.m, dtype=self.torch_dtype, device=self.device)
         if scratch.numel() < self.n * self.m:
@@ -93,7 +109,7 @@ class PoetxLinear:
         self.W = scratch[: self.n * self.m].view(self.n, self.m)
 
     def _dequantize(self, stream=None) -> None:
-        if self.Wq is not None:
+        if self.Wq is not None and not self.int8_product:
             self.W = self._wscratch[: self.n * self.m].view(self.n, self.m)
             poetx_weight_dequantize(self.n, self.m, self.Wq, self.Wscale, self.dtype, self.W, stream)
 
@@ -130,7 +146,25 @@ class PoetxLinear:
         poetx_frame_import(self.abi(), W0lin, stream)
         self.build(stream)
 
+    def _need_weight(self, what: str) -> None:
+        if self.int8_product:
+            raise RuntimeError(f"{what}: the layer keeps its weight as int8 codes only (int8_product)")
+
+    def _q8(self, y, xg):
+        """The poetx_q8 of a call with these saved activations, or None."""
+        y8, xg8 = isinstance(y, Checkpoint), isinstance(xg, Checkpoint)
+        if not (y8 or xg8 or self.int8_product):
+            return None
+        return make_q8(self.Wq if self.int8_product else None, self.Wscale if self.int8_product else None,
+                       y.codes if y8 else None, y.exps if y8 else None, xg.codes if xg8 else None,
+                       xg.exps if xg8 else None)
+
+    def _new_checkpoint(self, T: int, d: int) -> Checkpoint:
+        return Checkpoint(torch.empty((T, d), dtype=torch.int8, device=self.device),
+                          torch.empty((T, (d + 31) // 32), dtype=torch.uint8, device=self.device))
+
     def export_weight(self, stream=None) -> torch.Tensor:
+        self._need_weight("export_weight")
         out = torch.empty((self.n, self.m), dtype=self.torch_dtype, device=self.device)
         poetx_frame_export(self.abi(), out, stream)
         return out
@@ -145,31 +179,54 @@ class PoetxLinear:
     # -------------------------------------------------------------- layer
     def forward(self, x: torch.Tensor, save: bool = True, save_xg: bool = False, z: Optional[torch.Tensor] = None,
                 y: Optional[torch.Tensor] = None, xg: Optional[torch.Tensor] = None,
-                stream=None) -> Tuple[torch.Tensor, Optional["Saved"]]:
+                stream=None, save8: bool = False) -> Tuple[torch.Tensor, Optional["Saved"]]:
         """z = x R W0 P.  With `save`, also returns what the backward needs:
-        Y (the P-side input) and, with `save_xg`, Xg = x[:, permR]."""
+        Y (the P-side input) and, with `save_xg`, Xg = x[:, permR].  With
+        `save8` both are kept as 8-bit checkpoints (int8 codes and an exponent
+        per 32 columns, about half the bytes; y and xg, if given, are
+        Checkpoints to write into): z is the same, and so is the backward's
+        dx, while the gradients of the triangles see the checkpoints' values."""
         T = x.shape[0]
         td = self.torch_dtype
         _need(x, (T, self.m), td, self.device, "x")
         if z is None:
             z = torch.empty((T, self.n), dtype=td, device=self.device)
         _need(z, (T, self.n), td, self.device, "z")
+        if save8 and self.fold:
+            raise ValueError("save8: the layer folds its blocks into the weight (fold != 0)")
         if save and y is None:
-            y = torch.empty((T, self.n), dtype=td, device=self.device)
-        if save:
-            _need(y, (T, self.n), td, self.device, "y")
+            y = (self._new_checkpoint(T, self.n) if save8 else
+                 torch.empty((T, self.n), dtype=td, device=self.device))
         if save and save_xg and xg is None:
-            xg = torch.empty((T, self.m), dtype=td, device=self.device)
-        if not (save and save_xg):
-            xg = None
-        if xg is not None:
-            _need(xg, (T, self.m), td, self.device, "xg")
+            xg = (self._new_checkpoint(T, self.m) if save8 else
+                  torch.empty((T, self.m), dtype=td, device=self.device))
+        y = y if save else None
+        xg = xg if save and save_xg else None
+        for name, t, d in (("y", y, self.n), ("xg", xg, self.m)):
+            if t is not None:
+                self._need_saved(t, T, d, name, save8)
         self._dequantize(stream)
         L = self.abi()
-        nb = poetx_forward_workspace_bytes(L, T)
-        ws = self.workspace("fwd", nb)
-        poetx_forward(L, T, x, z, y if save else None, xg, ws, nb, stream)
+        q8 = self._q8(y, xg)
+        if q8 is None:
+            nb = poetx_forward_workspace_bytes(L, T)
+            ws = self.workspace("fwd", nb)
+            poetx_forward(L, T, x, z, y, xg, ws, nb, stream)
+        else:
+            nb = poetx_forward_q8_workspace_bytes(L, T, q8)
+            ws = self.workspace("fwd", nb)
+            poetx_forward_q8(L, T, x, z, None if save8 else y, None if save8 else xg, q8, ws, nb, stream)
         return z, (Saved(y, xg) if save else None)
+
+    def _need_saved(self, t, T: int, d: int, name: str, as_checkpoint: bool) -> None:
+        if as_checkpoint != isinstance(t, Checkpoint):
+            raise TypeError(f"{name}: expected a {'Checkpoint' if as_checkpoint else 'torch.Tensor'}, "
+                            f"got {type(t).__name__}")
+        if as_checkpoint:
+            _need(t.codes, (T, d), torch.int8, self.device, f"{name} codes")
+            _need(t.exps, (T, (d + 31) // 32), torch.uint8, self.device, f"{name} exps")
+        else:
+            _need(t, (T, d), self.torch_dtype, self.device, name)
 
     def backward(self, x: torch.Tensor, saved, dz: torch.Tensor, need_dx: bool = True,
                  dx: Optional[torch.Tensor] = None, dqR: Optional[torch.Tensor] = None,
@@ -179,7 +236,7 @@ class PoetxLinear:
         which keeps no [T][n] activation between forward and backward)."""
         if saved is None:
             saved = Saved(None, None)
-        elif isinstance(saved, torch.Tensor):
+        elif isinstance(saved, (torch.Tensor, Checkpoint)):
             saved = Saved(saved, None)
         T = dz.shape[0]
         if need_dx and dx is None:
@@ -192,10 +249,7 @@ class PoetxLinear:
         _need(dqR, tuple(self.qR.shape), torch.float32, self.device, "dqR")
         _need(dqP, tuple(self.qP.shape), torch.float32, self.device, "dqP")
         self._dequantize(stream)
-        L = self.abi()
-        nb = (poetx_backward_workspace_bytes if saved.y is not None else poetx_backward_recompute_workspace_bytes)(L, T)
-        ws = self.workspace("bwd", nb)
-        poetx_backward(L, T, x, saved.y, saved.xg, dz, dx if need_dx else None, dqR, dqP, int(accumulate), ws, nb,
+        self._backward(poetx_backward, poetx_backward_q8, T, x, saved, dz, dx if need_dx else None, dqR, dqP, accumulate,
                        stream)
         return (dx if need_dx else None), dqR, dqP
 
@@ -207,7 +261,7 @@ class PoetxLinear:
         of all layers into dq in one batch."""
         if saved is None:
             saved = Saved(None, None)
-        elif isinstance(saved, torch.Tensor):
+        elif isinstance(saved, (torch.Tensor, Checkpoint)):
             saved = Saved(saved, None)
         T = dz.shape[0]
         if need_dx and dx is None:
@@ -216,12 +270,23 @@ class PoetxLinear:
         _need(dGR, (self.m // self.b, self.b, self.b), torch.float32, self.device, "dGR")
         _need(dGP, (self.n // self.b, self.b, self.b), torch.float32, self.device, "dGP")
         self._dequantize(stream)
-        L = self.abi()
-        nb = (poetx_backward_workspace_bytes if saved.y is not None else poetx_backward_recompute_workspace_bytes)(L, T)
-        ws = self.workspace("bwd", nb)
-        poetx_backward_dG(L, T, x, saved.y, saved.xg, dz, dx if need_dx else None, dGR, dGP, int(accumulate), ws, nb,
-                          stream)
+        self._backward(poetx_backward_dG, poetx_backward_dG_q8, T, x, saved, dz, dx if need_dx else None, dGR, dGP,
+                       accumulate, stream)
         return dx if need_dx else None
+
+    def _backward(self, call, call_q8, T: int, x, saved: "Saved", dz, dx, gR, gP, accumulate: bool, stream) -> None:
+        L = self.abi()
+        q8 = self._q8(saved.y, saved.xg)
+        y = None if isinstance(saved.y, Checkpoint) else saved.y
+        xg = None if isinstance(saved.xg, Checkpoint) else saved.xg
+        if q8 is None:
+            nb = (poetx_backward_workspace_bytes if y is not None else poetx_backward_recompute_workspace_bytes)(L, T)
+            ws = self.workspace("bwd", nb)
+            call(L, T, x, y, xg, dz, dx, gR, gP, int(accumulate), ws, nb, stream)
+        else:
+            nb = poetx_backward_q8_workspace_bytes(L, T, int(y is not None), q8)
+            ws = self.workspace("bwd", nb)
+            call_q8(L, T, x, y, xg, q8, dz, dx, gR, gP, int(accumulate), ws, nb, stream)
 
     def _check_backward(self, T: int, x, saved: "Saved", dz, dx) -> None:
         td = self.torch_dtype
@@ -230,16 +295,18 @@ class PoetxLinear:
             _need(x, (T, self.m), td, self.device, "x")
         elif saved.xg is None:
             raise ValueError("x: needed unless the forward saved Xg")
-        if saved.y is not None:
-            _need(saved.y, (T, self.n), td, self.device, "saved y")
-        if saved.xg is not None:
-            _need(saved.xg, (T, self.m), td, self.device, "saved xg")
+        if self.fold and (isinstance(saved.y, Checkpoint) or isinstance(saved.xg, Checkpoint)):
+            raise ValueError("saved: checkpoints, but the layer folds its blocks into the weight (fold != 0)")
+        for name, t, d in (("saved y", saved.y, self.n), ("saved xg", saved.xg, self.m)):
+            if t is not None:
+                self._need_saved(t, T, d, name, isinstance(t, Checkpoint))
         if dx is not None:
             _need(dx, (T, self.m), td, self.device, "dx")
 
     def merge(self, new_permR: torch.Tensor, new_permP: torch.Tensor, stream=None) -> None:
         """W0 <- R W0 P, re-expressed in the frame of the new permutations;
         q = 0 and G = I afterwards."""
+        self._need_weight("merge")
         L = self.abi()
         nb = poetx_merge_workspace_bytes(L)
         ws = self.workspace("merge", nb)
@@ -252,6 +319,50 @@ class PoetxLinear:
         self.W = W_out
         self.permR.copy_(newR)
         self.permP.copy_(newP)
+
+
+class Int8Linear:
+    """A linear z = x W^T served in 8 bits: the weight as int8 codes with a
+    scale per row, tokens as int8 rows (rmsnorm_quantize or quantize_rows), the
+    product in int8.  from_layer takes a trained POET-X layer with its R and P
+    folded into the weight; the layer itself stays as it is."""
+
+    def __init__(self, W: torch.Tensor, stream=None):
+        if not isinstance(W, torch.Tensor) or W.dim() != 2 or W.dtype not in _TORCH_DTYPE.values():
+            raise ValueError("W: expected a [n][m] torch.bfloat16 or torch.float32 tensor")
+        if not W.is_contiguous():
+            raise ValueError("W: must be contiguous")
+        self.n, self.m = W.shape
+        self.dtype = W.dtype
+        self.Wq = torch.empty((self.n, self.m), dtype=torch.int8, device=W.device)
+        self.wscale = torch.empty(self.n, dtype=torch.float32, device=W.device)
+        code = next(k for k, v in _TORCH_DTYPE.items() if v == W.dtype)
+        poetx_weight_quantize(self.n, self.m, W, code, self.Wq, self.wscale, stream)
+
+    @classmethod
+    def from_layer(cls, layer: PoetxLinear, stream=None) -> "Int8Linear":
+        layer._need_weight("from_layer")
+        layer._dequantize(stream)
+        # merge a copy of the layer's state into the natural order (identity permutations)
+        keep = [t.clone() for t in (layer.qR, layer.qP, layer.GR, layer.GP)]
+        L = make_layer(layer.m, layer.n, layer.b, layer.dtype, layer.W, layer.permR, layer.permP, *keep)
+        eyeR = torch.arange(layer.m, dtype=torch.int32, device=layer.device)
+        eyeP = torch.arange(layer.n, dtype=torch.int32, device=layer.device)
+        W = torch.empty((layer.n, layer.m), dtype=layer.torch_dtype, device=layer.device)
+        nb = poetx_merge_workspace_bytes(L)
+        ws = torch.empty(max(nb, 1), dtype=torch.uint8, device=layer.device)
+        poetx_merge(L, eyeR, eyeP, W, ws, nb, stream)
+        return cls(W, stream)
+
+    def forward(self, x) -> torch.Tensor:
+        """z [T][n] from tokens [T][m] (quantized here) or from their int8 rows
+        (anything with .codes and .scale: QuantRows, NormRows)."""
+        rows = quantize_rows(x) if isinstance(x, torch.Tensor) else x
+        return matmul_int8(rows.codes, rows.scale, self.Wq, self.wscale, self.dtype)
+
+    def backward(self, dz: torch.Tensor) -> torch.Tensor:
+        """dx [T][m] of the tokens from dz [T][n], in 8 bits too."""
+        return matmul_int8_grad(dz, self.Wq, self.wscale)
 
 
 class LayerGroup:

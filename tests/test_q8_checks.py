@@ -1,5 +1,7 @@
 """The 8-bit operators refuse what they cannot take before anything is queued:
 the C calls by status, the torch functions by exception (no GPU needed)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -125,3 +127,29 @@ def test_torch_functions_refuse():
         px.block_backward(ck, x, torch.zeros(1, 64, 32, dtype=BF))
     with pytest.raises(ValueError, match="G: dtype"):
         px.block_backward(ck, x, torch.zeros(1, 64, 64))
+
+
+def test_statuses_of_the_layer_in_8_bits(lib):
+    L = px.poetx_layer(512, 256, 64, px.POETX_BF16, P, P, P, P, P, P, P, 0)
+    folded = px.poetx_layer(512, 256, 64, px.POETX_BF16, P, P, P, P, P, P, P, 1)
+    q = px.poetx_q8(P, P, P, P, P, P)
+    need = px.poetx_forward_q8_workspace_bytes(L, 10, q)
+    assert need > px.poetx_forward_workspace_bytes(L, 10)
+    assert px.poetx_backward_q8_workspace_bytes(L, 10, 0, q) > px.poetx_backward_workspace_bytes(L, 10)
+    assert px.poetx_forward_q8_workspace_bytes(folded, 10, q) == 0
+    f = lambda l, z, y, xg, q8, ws: lib.poetx_forward_q8(ctypes.byref(l), 10, P, z, y, xg, ctypes.byref(q8), P, ws, None)  # noqa: E731
+    assert f(folded, P, None, None, q, need) == 1
+    assert f(L, P, P, None, q, need) == 1                                   # Y in both forms
+    assert f(L, P, None, P, q, need) == 1
+    assert f(L, P, None, None, q, need - 1) == 5
+    assert f(L, P, None, None, px.poetx_q8(P, None, None, None, None, None), need) == 1   # codes without scales
+    assert f(L, P, None, None, px.poetx_q8(None, None, P, None, None, None), need) == 1
+    assert f(L, P, None, None, px.poetx_q8(None, None, ODD, P, None, None), need) == 4
+    assert lib.poetx_forward_q8(ctypes.byref(L), 10, P, P, None, None, None, P, need, None) == 1
+    nb = px.poetx_backward_q8_workspace_bytes(L, 10, 0, q)
+    b = lib.poetx_backward_q8
+    assert b(ctypes.byref(L), 10, P, P, None, ctypes.byref(q), P, None, P, P, 0, P, nb, None) == 1
+    assert b(ctypes.byref(L), 10, P, None, None, ctypes.byref(q), P, None, P, P, 0, P, nb - 1, None) == 5
+    assert b(ctypes.byref(L), 10, P, None, None, ctypes.byref(q), None, None, P, P, 0, P, nb, None) == 1
+    assert lib.poetx_backward_dG_q8(ctypes.byref(L), 10, P, None, None, ctypes.byref(q), P, None, None, P, 0, P, nb,
+                                    None) == 1
