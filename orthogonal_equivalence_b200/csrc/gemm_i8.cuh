@@ -419,18 +419,48 @@ __global__ void __launch_bounds__(NUM_THREADS)
     }
   }
   if (S > 1) {
-    // add the S integer sums of the tile: this CTA the token columns rank, rank + S, ...
+    // add the S integer sums of the tile: this CTA the token columns rank,
+    // rank + S, ..., a warp one of them at a time, four weight rows a lane; all
+    // S reads of a column are in flight together
     tc2::cluster_sync();
-    if (warp >= 2 && row_in) {
-      const uint32_t mine = smem_u32(part) + row * 4;
-      for (int c = rank; c < cols; c += S) {
-        int sum = 0;
-        for (int s = 0; s < S; ++s) {
-          int v;
-          asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(tc2::map_to_rank(mine + c * 512, s)) : "memory");
-          sum += v;
+    if (warp >= 2) {
+      const int j = n0 + lane * 4;
+      const bool whole = p.N % 4 == 0 && j < p.N;  // (then all four rows are inside)
+      float b[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) b[e] = p.bs && j + e < p.N ? p.bs[j + e] : 1.f;
+      const uint32_t mine = smem_u32(part) + lane * 16;
+      for (int c = rank + S * (warp - 2); c < cols; c += 4 * S) {
+        int v[8][4];
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+          if (s < S)
+            asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v[s][0]), "=r"(v[s][1]), "=r"(v[s][2]), "=r"(v[s][3])
+                         : "r"(tc2::map_to_rank(mine + c * 512, s))
+                         : "memory");
+          else v[s][0] = v[s][1] = v[s][2] = v[s][3] = 0;
         }
-        out[static_cast<int64_t>(c) * p.N + row] = from_f32<T>(static_cast<float>(sum) * __ldg(as + c) * bs);
+        const float a = __ldg(as + c);
+        float o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          int sum = 0;
+#pragma unroll
+          for (int s = 0; s < 8; ++s) sum += v[s][e];
+          o[e] = static_cast<float>(sum) * a * b[e];
+        }
+        T* dst = out + static_cast<int64_t>(c) * p.N + lane * 4;
+        if (whole) {
+          if constexpr (sizeof(T) == 2)
+            *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+          else
+            *reinterpret_cast<float4*>(dst) = make_float4(o[0], o[1], o[2], o[3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (j + e < p.N) dst[e] = from_f32<T>(o[e]);
+        }
       }
     }
     tc2::cluster_sync();  // no CTA leaves while its sums are read
