@@ -297,6 +297,13 @@ struct WideParams {
   int tmem_cols;
 };
 
+// Programmatic dependent launch: a kernel launched with that attribute may
+// start, and set up its barriers and TMEM, once every CTA of the kernel before
+// it has called grid_launch or ended; grid_wait returns when that kernel has
+// completed and its writes are visible.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Grid (S, ceil(N / 128), ceil(T / nt)), clusters of the S CTAs of one tile.
 // CTA s takes the K blocks [s nkb / S, (s + 1) nkb / S), S <= nkb.  For a few
 // tokens the weight's bytes bound it: 1 x 4096 -> 14336 takes 13.2 us (9.0 at
@@ -339,6 +346,9 @@ __global__ void __launch_bounds__(NUM_THREADS)
     mbar_init(done, 1);
     fence_barrier_init();
     fence_async_smem();
+    prefetch_tmap(&tmW);
+    prefetch_tmap(&tmX);
+    grid_wait();
     // the first round of loads flies while TMEM is allocated
     for (int kb = k_first; kb < k_early; ++kb) load(kb, kb - k_first);
   }
@@ -350,6 +360,8 @@ __global__ void __launch_bounds__(NUM_THREADS)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
+  grid_wait();    // before any thread reads or writes what earlier kernels of the stream do
+  grid_launch();  // the next kernel may set itself up
 
   if (warp == 0) {
     if (lane == 0) {

@@ -1276,13 +1276,15 @@ cudaError_t launch_wide_i8(const ProductI8& q, const WideShape& w, cudaStream_t 
   cfg.blockDim = dim3(i8::NUM_THREADS);
   cfg.dynamicSmemBytes = size_t(w.stages) * (i8::BOX_BYTES + w.nt * i8::KB) + 1024 + 256;
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = w.S;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, i8::product_wide_kernel<T>, mw, mx, p);
 }
 
@@ -1339,25 +1341,27 @@ cudaError_t launch_pair_i8(const ProductI8& q, cudaStream_t st, int device) {
 // Up to 64 tokens take the narrowest tile that holds them.  Beyond, a tile of
 // 64 tokens as long as two CTAs a SM hold them all, then one of 128, then the
 // pair kernel; in us (64, 128, pair), product of T tokens by [n][m]:
-//   333 x 4096 -> 1024:  12, 14, 24     512 x 4096 -> 4096:  18, 20, 26
-//   1024 x 4096 -> 4096: 28, 23, 26     256 x 4096 -> 14336: 27, 24, 28
-//   512 x 4096 -> 14336: 50, 44, 40     1111 x 5120 -> 13824: 118, 99, 68
-// K is split over 2, 4 or 8 CTAs while they all stay resident (four narrow
-// CTAs a SM, else two, and not where the tiles alone fill half the SMs: 200 x
-// 4096 -> 4096 takes 16 us whole, 17 in two); 3, 5 or 6 fit the GPCs badly (1 x
-// 4096 -> 14336: 13.2 us for four, 15.2 for five).
+//   333 x 4096 -> 1024:  9.7, 10.5, 24   512 x 4096 -> 4096:  17, 18, 26
+//   1024 x 4096 -> 4096: 28, 23, 26      256 x 4096 -> 14336: 27, 24, 28
+//   512 x 4096 -> 14336: 50, 44, 40      1111 x 5120 -> 13824: 118, 99, 68
+// A long K (512 x 14336 -> 4096: 41, 35) pays for 128 sooner, split in two.
+// K is split over 2, 4 or 8 CTAs while they all stay resident, four narrow
+// CTAs a SM, else two (200 x 4096 -> 4096: 15.9 us whole, 13.4 in two); 3, 5
+// or 6 fit the GPCs badly (1 x 4096 -> 14336: 12.7 us for four, 15 for five).
 WideShape wide_shape(int T, int N, int K, int device) {
   WideShape w{0, 1, 0};
   const int sms = sm_count(device);
   auto tiles_of = [&](int nt) { return int64_t((N + 127) / 128) * ((T + nt - 1) / nt); };
-  w.nt = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 || tiles_of(64) <= 2 * sms ? 64 : T <= 128 || tiles_of(128) <= 2 * sms ? 128 : 0;
-  if (w.nt == 0) return w;
-  const int64_t tiles = tiles_of(w.nt);
   const int nkb = (K + i8::KB - 1) / i8::KB;
-  const int64_t slots = w.nt <= 32 ? 4 * sms : tiles <= sms / 2 ? 2 * sms : 0;
-  while (w.S < 8 && 2 * w.S * tiles <= slots && 4 * w.S <= nkb) w.S *= 2;
-  const int64_t per = (tiles * w.S + sms - 1) / sms;  // CTAs a SM
-  const int per_sm = per > (w.nt <= 32 ? 4 : 2) ? (w.nt <= 32 ? 4 : 2) : static_cast<int>(per);
+  if (T <= 64) w.nt = T <= 16 ? 16 : T <= 32 ? 32 : 64;
+  else if (tiles_of(64) <= 2 * sms) w.nt = nkb >= 64 && tiles_of(64) > sms && tiles_of(128) <= sms ? 128 : 64;
+  else if (T <= 128 || tiles_of(128) <= 2 * sms) w.nt = 128;
+  else return w;
+  const int64_t tiles = tiles_of(w.nt);
+  const int most = w.nt <= 32 ? 4 : 2;  // CTAs a SM holds
+  while (w.S < 8 && 2 * w.S * tiles <= int64_t(most) * sms && 4 * w.S <= nkb) w.S *= 2;
+  const int64_t per = (tiles * w.S + sms - 1) / sms;
+  const int per_sm = per > most ? most : static_cast<int>(per);
   const int stage = i8::BOX_BYTES + w.nt * i8::KB;
   w.stages = (228 * 1024 / per_sm - 1024 - 1280) / stage;  // 1 KB of the SM's 228 goes to the system for each CTA
   if (w.stages > 8) w.stages = 8;
