@@ -6,7 +6,7 @@
 // as in bdg2sm.cuh, except that X [T][d] is read as int8 codes with one
 // exponent per 32 columns (q8.cuh): 1.03 bytes an element instead of 2, and no
 // bf16 copy of X in memory.  The tensor cores have no int8 x bf16 product, so
-// four warps turn the codes into the bf16 operand tile in shared memory; code *
+// eight warps turn the codes into the bf16 operand tile in shared memory; code *
 // 2^e is exact in bf16, so the product sees the checkpoint's own values.
 //
 // A pair of SMs takes a work item (block j, token split s) and walks its
@@ -24,8 +24,8 @@
 //   warp 0: TMA producer (both CTAs)
 //   warp 1: TMEM owner (both CTAs) and MMA issuer (leader only)
 //   warps 2-5: epilogues (both CTAs)
-//   warps 6-9: codes -> bf16 (both CTAs)
-//   warp 10: TMA producer of the codes (both CTAs)
+//   warps 6-13: codes -> bf16 (both CTAs)
+//   warp 14: TMA producer of the codes (both CTAs)
 //
 // The arrivals at the leader's barriers that stand for shared-memory writes or
 // TMEM reads of this SM use the plain remote arrive: after the proxy fence (or
@@ -33,6 +33,12 @@
 // only place the pair's MMA reads it from, so nothing has to be released to the
 // rest of the cluster.  A release at cluster scope waits for the memory system:
 // with one per chunk and warp the kernel took 155 us instead of 120.
+//
+// 16384 x 4096 takes 87 us with the sum of the splits, 63 us without O (53 and
+// 32 us at the copy rate).  Neither HBM (41%) nor the tensor pipe (39%) is the
+// bound: a chunk's way from codes to MMA and back is, through the converting
+// warps (four of them: 96 us) and the rings' hand-overs; deeper rings of any of
+// the three operands change nothing.
 // Every wait is bounded (ptx.cuh).  No load uses multicast.
 #pragma once
 
@@ -54,11 +60,12 @@ using bdg2::HALF;
 using bdg2::TILE_BYTES;
 using bdg2::UMMA_K;
 constexpr int UNITS = 4;                        // ring of D units (TILE_BYTES each)
-constexpr int XUNITS = 3;                       // converted X
-constexpr int SLOTS = 2;                        // codes
+constexpr int XUNITS = 2;                       // converted X
+constexpr int SLOTS = 4;                        // codes
 constexpr int SLOT_BYTES = CH * HALF;           // 64 tokens x 128 codes
 constexpr int SMEM_BYTES = (UNITS + XUNITS) * TILE_BYTES + SLOTS * SLOT_BYTES + G_BYTES + EPI_BYTES + 1024 + 320;
-constexpr int NUM_THREADS = 352;
+constexpr int NUM_THREADS = 480;
+constexpr int CONV_WARPS = 8;
 constexpr int SPLIT_TOKENS = 2048;              // most tokens of a split (see above), about
 
 struct Params {
@@ -147,12 +154,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       mbar_init(bar(EMPTY + s), 1);
     }
     for (int s = 0; s < XUNITS; ++s) {
-      mbar_init(bar(XFULL + s), 8);   // 4 converting warps x 2 CTAs
+      mbar_init(bar(XFULL + s), 2 * CONV_WARPS);  // of both CTAs
       mbar_init(bar(XEMPTY + s), 1);
     }
     for (int s = 0; s < SLOTS; ++s) {
       mbar_init(bar(CFULL + s), 1);
-      mbar_init(bar(CEMPTY + s), 4);
+      mbar_init(bar(CEMPTY + s), CONV_WARPS);
     }
     mbar_init(bar(GFULL), 1);
     mbar_init(bar(GEMPTY), 1);
@@ -292,7 +299,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         tc2::commit_pair(bar(AFULL));                  // also: every MMA of the item is done
       }
     }
-  } else if (warp == 10) {
+  } else if (warp == 6 + CONV_WARPS) {
     if (lane == 0) {
       // ---------------- TMA producer of the codes (both CTAs)
       prefetch_tmap(&tmX);
@@ -317,21 +324,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       }
     }
   } else if (warp >= 6) {
-    // ---------------- codes -> bf16 (both CTAs): thread = (token of the chunk, half of the columns)
+    // ---------------- codes -> bf16 (both CTAs): thread = (token of the chunk, group of 32 columns)
     const int ct = threadIdx.x - 192;
-    const int row = ct & 63, half = ct >> 6;
+    const int row = ct & 63, group = ct >> 6;
     const uint32_t xfull_leader = tc2::map_to_rank(bar(XFULL), 0);
-    // The two exponents of this thread's row in each chunk of a tile, loaded a
+    // The exponent of this thread's group in each chunk of a tile, loaded a
     // tile ahead (rows behind the last token: 0, which reads as 0 like their
     // codes).
     uint32_t ex[4];
     auto exponents_of = [&](int item) {  // of the item's block, first row of this thread
-      return pp.exps + ((item % p.nblk) * BLK + int(rank) * HALF + half * CH) / q8::GROUP + int64_t(row) * pp.ng;
+      return pp.exps + ((item % p.nblk) * BLK + int(rank) * HALF) / q8::GROUP + group + int64_t(row) * pp.ng;
     };
     auto exponents = [&](const uint8_t* of, int token0, int c) {
       ex[c] = token0 + c * CH + row < p.T
-                  ? __ldg(reinterpret_cast<const unsigned short*>(of + int64_t(token0 + c * CH) * pp.ng))
-                  : 0;
+                  ? __ldg(of + int64_t(token0 + c * CH) * pp.ng) : 0;
     };
     int u = 0, slot = 0;
     uint32_t ring = 0, cring = 0;
@@ -359,29 +365,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                mbar_wait(bar(XEMPTY + u), ring ^ 1u, DERR_GEMM_WAIT);
           ok = __all_sync(0xffffffffu, ok);
           if (ok) {
-            const float s0 = q8::exponent_value(ex[c] & 0xffu), s1 = q8::exponent_value(ex[c] >> 8);
+            const float sc = q8::exponent_value(ex[c]);
             exponents(of, next0, c);
             const uint32_t src = sCode + slot * SLOT_BYTES + row * 128;
-            const uint32_t dst = sX + u * TILE_BYTES + half * (CH * 128) + row * 128;
-            uint32_t w[4][4];
+            const uint32_t dst = sX + u * TILE_BYTES + (group >> 1) * (CH * 128) + row * 128;
+            const int d0 = (group & 1) * 4;  // this group's first 16-byte unit in the row of 64 columns
+            uint32_t w[2][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 2; ++i)
               asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                            : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
-                           : "r"(src + (((half * 4 + i) ^ (row & 7)) << 4))
+                           : "r"(src + (((group * 2 + i) ^ (row & 7)) << 4))
                            : "memory");
             auto put = [&](auto far) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
+              for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                  const uint4 o = expand8<decltype(far)::value>(w[i][2 * h], w[i][2 * h + 1], i < 2 ? s0 : s1);
-                  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (((2 * i + h) ^ (row & 7)) << 4)),
+                  const uint4 o = expand8<decltype(far)::value>(w[i][2 * h], w[i][2 * h + 1], sc);
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                   dst + (((d0 + 2 * i + h) ^ (row & 7)) << 4)),
                                "r"(o.x), "r"(o.y), "r"(o.z), "r"(o.w)
                                : "memory");
                 }
             };
-            if (s0 >= 0x1p100f || s1 >= 0x1p100f) put(std::true_type());
+            if (sc >= 0x1p100f) put(std::true_type());
             else put(std::false_type());
             fence_async_smem();
             __syncwarp();
@@ -416,26 +424,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           tc_fence_after();
           const int row0 = tile * BLK + int(rank) * HALF + quarter * 32;  // token rows of this warp
           const bool rows_in = row0 < p.T;
-          // the whole 256-column row into registers (bf16 pairs), then release
-          // the accumulator so the next tile's MMA1 can start while this tile
-          // is stored
-          uint32_t w[BLK / 2];
+          // half a row at a time into registers (bf16 pairs) and out through the
+          // boxes; the accumulator is released once the second half is read
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            uint32_t w[BLK / 4];
 #pragma unroll
-          for (int c = 0; c < BLK / 64; ++c) {
-            float v[32];  // (one load at a time: 320 threads leave 200 registers each)
+            for (int g = 0; g < 4; ++g) {
+              float v[32];
+              tmem_ld_32cols(tl + 128 * h + 32 * g, v);
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              tmem_ld_32cols(tl + 64 * c + 32 * g, v);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) w[32 * c + 16 * g + i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+              for (int i = 0; i < 16; ++i) w[16 * g + i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
             }
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) arrive_pair(oempty_leader);
-          if (rows_in) {
+            if (h == 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) arrive_pair(oempty_leader);
+            }
+            if (!rows_in) continue;
 #pragma unroll
-            for (int c0 = 0; c0 < BLK / 64; ++c0) {
+            for (int c0 = 0; c0 < 2; ++c0) {
               if (lane == 0) bulk_wait_read<1>();
               __syncwarp();
               const uint32_t box = my_boxes + buf * EPI_BOX;
@@ -449,7 +457,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
               fence_async_smem();
               __syncwarp();
               if (lane == 0) {
-                tma_store_2d(&tmO, box, j * BLK + 64 * c0, row0);
+                tma_store_2d(&tmO, box, j * BLK + 128 * h + 64 * c0, row0);
                 bulk_commit();
               }
               buf ^= 1;
