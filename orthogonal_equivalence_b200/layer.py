@@ -89,6 +89,7 @@ class PoetxLinear:
         the codes themselves with its other operand quantized row by row (see
         poetx_q8 in include/poetx.h); merge and export need the weight and
         refuse then."""
+        self._need_weight("quantize_weight")
         if int8_product and self.fold:
             raise ValueError("int8_product: the layer folds its blocks into the weight (fold != 0)")
         if int8_product and scratch is not None:
@@ -118,6 +119,10 @@ class PoetxLinear:
         return _TORCH_DTYPE[self.dtype]
 
     def abi(self):
+        self._need_weight("abi")
+        return self._abi()
+
+    def _abi(self):
         return make_layer(self.m, self.n, self.b, self.dtype, self.W, self.permR, self.permP, self.qR, self.qP,
                           self.GR, self.GP, self.fold)
 
@@ -139,6 +144,10 @@ class PoetxLinear:
                                ("qR", qR, self.qR.shape), ("qP", qP, self.qP.shape)):
             if tuple(t.shape) != tuple(shape):
                 raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if self.int8_product:  # back to a layer that has its weight
+            self.W = torch.empty((self.n, self.m), dtype=self.torch_dtype, device=self.device)
+            self.Wq = self.Wscale = None
+            self.int8_product = False
         self.permR.copy_(permR)
         self.permP.copy_(permP)
         self.qR.copy_(qR)
@@ -171,7 +180,7 @@ class PoetxLinear:
 
     def build(self, stream=None) -> None:
         """G_R, G_P from qR, qP (Cayley-Neumann), both sides in one batch."""
-        L = self.abi()
+        L = self._abi()
         nb = poetx_layer_cnp_workspace_bytes(L)
         ws = self.workspace("cnp", nb)
         poetx_layer_cnp_build(L, ws, nb, stream)
@@ -206,7 +215,7 @@ class PoetxLinear:
             if t is not None:
                 self._need_saved(t, T, d, name, save8)
         self._dequantize(stream)
-        L = self.abi()
+        L = self._abi()
         q8 = self._q8(y, xg)
         if q8 is None:
             nb = poetx_forward_workspace_bytes(L, T)
@@ -215,7 +224,8 @@ class PoetxLinear:
         else:
             nb = poetx_forward_q8_workspace_bytes(L, T, q8)
             ws = self.workspace("fwd", nb)
-            poetx_forward_q8(L, T, x, z, None if save8 else y, None if save8 else xg, q8, ws, nb, stream)
+            with torch.cuda.device(x.device):
+                poetx_forward_q8(L, T, x, z, None if save8 else y, None if save8 else xg, q8, ws, nb, stream)
         return z, (Saved(y, xg) if save else None)
 
     def _need_saved(self, t, T: int, d: int, name: str, as_checkpoint: bool) -> None:
@@ -275,7 +285,7 @@ class PoetxLinear:
         return dx if need_dx else None
 
     def _backward(self, call, call_q8, T: int, x, saved: "Saved", dz, dx, gR, gP, accumulate: bool, stream) -> None:
-        L = self.abi()
+        L = self._abi()
         q8 = self._q8(saved.y, saved.xg)
         y = None if isinstance(saved.y, Checkpoint) else saved.y
         xg = None if isinstance(saved.xg, Checkpoint) else saved.xg
@@ -286,7 +296,8 @@ class PoetxLinear:
         else:
             nb = poetx_backward_q8_workspace_bytes(L, T, int(y is not None), q8)
             ws = self.workspace("bwd", nb)
-            call_q8(L, T, x, y, xg, q8, dz, dx, gR, gP, int(accumulate), ws, nb, stream)
+            with torch.cuda.device(dz.device):
+                call_q8(L, T, x, y, xg, q8, dz, dx, gR, gP, int(accumulate), ws, nb, stream)
 
     def _check_backward(self, T: int, x, saved: "Saved", dz, dx) -> None:
         td = self.torch_dtype
@@ -332,12 +343,15 @@ class Int8Linear:
             raise ValueError("W: expected a [n][m] torch.bfloat16 or torch.float32 tensor")
         if not W.is_contiguous():
             raise ValueError("W: must be contiguous")
+        if W.device.type != "cuda":
+            raise ValueError(f"W: tensor on {W.device}: the library runs on CUDA devices")
         self.n, self.m = W.shape
         self.dtype = W.dtype
         self.Wq = torch.empty((self.n, self.m), dtype=torch.int8, device=W.device)
         self.wscale = torch.empty(self.n, dtype=torch.float32, device=W.device)
         code = next(k for k, v in _TORCH_DTYPE.items() if v == W.dtype)
-        poetx_weight_quantize(self.n, self.m, W, code, self.Wq, self.wscale, stream)
+        with torch.cuda.device(W.device):
+            poetx_weight_quantize(self.n, self.m, W, code, self.Wq, self.wscale, stream)
 
     @classmethod
     def from_layer(cls, layer: PoetxLinear, stream=None) -> "Int8Linear":
@@ -351,7 +365,8 @@ class Int8Linear:
         W = torch.empty((layer.n, layer.m), dtype=layer.torch_dtype, device=layer.device)
         nb = poetx_merge_workspace_bytes(L)
         ws = torch.empty(max(nb, 1), dtype=torch.uint8, device=layer.device)
-        poetx_merge(L, eyeR, eyeP, W, ws, nb, stream)
+        with torch.cuda.device(W.device):
+            poetx_merge(L, eyeR, eyeP, W, ws, nb, stream)
         return cls(W, stream)
 
     def forward(self, x) -> torch.Tensor:
@@ -441,7 +456,7 @@ class LayerGroup:
         poetx_cnp_backward(nblk, L0.b, self.q, dG, dq, int(accumulate), L0.dtype, self._bws, nb, stream)
 
     def build(self, stream=None) -> None:
-        abis = [L.abi() for L in self.layers]
+        abis = [L._abi() for L in self.layers]
         nb = poetx_layers_cnp_workspace_bytes(abis)
         if self._ws is None or self._ws.numel() < nb:
             self._ws = torch.empty(max(nb, 1), dtype=torch.uint8, device=self.layers[0].device)

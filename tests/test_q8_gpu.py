@@ -62,7 +62,7 @@ def quantise64(u):
 
 
 # ---------------------------------------------------------------- rows to int8
-ROWS = [(1, 1), (1, 4096), (3, 7), (5, 64), (77, 1000), (300, 1001), (130, 4096), (33, 5120), (9, 8200), (7, 14336),
+ROWS = [(1, 1), (1, 4096), (11, 9001), (3, 7), (5, 64), (77, 1000), (300, 1001), (130, 4096), (33, 5120), (9, 8200), (7, 14336),
         (5, 16383), (3, 20000), (2, 40001), (2, 102400)]
 
 
@@ -107,7 +107,7 @@ def test_quantize_rows_zero_and_nonfinite(d, dtype):
 
 
 # ---------------------------------------------------------------- norm
-NORM = [(1, 1), (1, 4096), (3, 7), (5, 64), (77, 1000), (300, 1001), (130, 4096), (33, 5120), (9, 8200), (7, 14336),
+NORM = [(1, 1), (1, 4096), (11, 9001), (3, 7), (5, 64), (77, 1000), (300, 1001), (130, 4096), (33, 5120), (9, 8200), (7, 14336),
         (5, 16383), (3, 20000), (2, 40001), (2, 51200)]
 EPS = 1e-5
 

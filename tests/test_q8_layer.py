@@ -131,6 +131,14 @@ def test_int8_weight_product_is_the_operators_sequence(dtype, m, n, b, T):
         L.merge(L.permR, L.permP)
     with pytest.raises(RuntimeError, match="export_weight"):
         L.export_weight()
+    with pytest.raises(RuntimeError, match="abi"):
+        L.abi()
+    with pytest.raises(RuntimeError, match="quantize_weight"):
+        L.quantize_weight()
+    px.LayerGroup([L]).build()                 # the blocks are still built
+    W0 = rnd(7, n, m, dtype=dtype)
+    L.load(W0, L.permR.clone(), L.permP.clone(), L.qR.clone(), L.qP.clone())   # and a new weight is a weight
+    assert not L.int8_product and torch.equal(L.export_weight(), W0)
 
 
 def test_int8_weight_product_is_near_the_bf16_layer():
@@ -224,3 +232,12 @@ def test_refusals_of_the_layer():
         px.poetx_backward_q8(L.abi(), 4, x, x, None, px.make_q8(y_codes=c.codes, y_exps=c.exps), x, None, L.qR, L.qP, 0,
                              ws, nb)
     assert e.value.status == 1
+
+
+def test_other_device_than_the_current_one():
+    if torch.cuda.device_count() < 2:
+        pytest.skip("one GPU")
+    with torch.cuda.device(1):
+        x = torch.randn(4, 64, device="cuda:1").to(BF)
+    q = px.quantize_rows(x)
+    assert q.codes.device == x.device
