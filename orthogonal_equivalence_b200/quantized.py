@@ -146,9 +146,9 @@ def rmsnorm_quantize(x: torch.Tensor, gamma: torch.Tensor, residual: Optional[to
         _like(residual, "residual", dt, x.shape, dev)
         h = torch.empty_like(x)
     q = torch.empty_like(x, dtype=torch.int8) if codes else None
-    s = torch.empty(T, dtype=torch.float32, device=dev) if codes else None
+    s = gamma.new_empty(T) if codes else None
     out = torch.empty_like(x) if y else None
-    rstd = torch.empty(T, dtype=torch.float32, device=dev)
+    rstd = gamma.new_empty(T)
     _run(dev, "poetx_rmsnorm_quantize", T, d, x.data_ptr(), _p(residual), gamma.data_ptr(), eps, _DTYPE[dt], _p(h),
          _p(out), _p(q), _p(s), rstd.data_ptr())
     return NormRows(q, s, x if h is None else h, rstd, out)
@@ -171,7 +171,7 @@ def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, gamma: torch.Tensor, rst
     if accumulate:
         _like(dgamma, "dgamma", torch.float32, (d,), dev)
     else:
-        dgamma = torch.empty(d, dtype=torch.float32, device=dev)
+        dgamma = torch.empty_like(gamma)
     dx = torch.empty_like(dy)
     nb = poetx_rmsnorm_backward_workspace_bytes(T, d, _DTYPE[dt])
     ws = torch.empty(nb, dtype=torch.uint8, device=dev)
@@ -192,7 +192,7 @@ def matmul_int8(xq: torch.Tensor, xscale: torch.Tensor, Wq: torch.Tensor, wscale
     _like(wscale, "wscale", torch.float32, (n,), dev)
     if dtype not in _DTYPE:
         raise ValueError(f"dtype: {dtype}, expected torch.bfloat16 or torch.float32")
-    out = torch.empty((T, n), dtype=dtype, device=dev)
+    out = torch.empty(T, n, dtype=dtype, device=dev)
     nb, ws = 0, None
     if m % 16:  # rows that are no whole 16-byte units are copied first
         nb = poetx_matmul_int8_workspace_bytes(T, n, m)
@@ -211,7 +211,7 @@ def matmul_int8_grad(dz: torch.Tensor, Wq: torch.Tensor, wscale: torch.Tensor) -
     if Wq.shape[0] != n or Wq.device != dev:
         _like(Wq, "Wq", torch.int8, (n, m), dev)
     _like(wscale, "wscale", torch.float32, (n,), dev)
-    dx = torch.empty((T, m), dtype=dz.dtype, device=dev)
+    dx = torch.empty(T, m, dtype=dz.dtype, device=dev)
     nb = poetx_matmul_int8_grad_workspace_bytes(T, n, m)
     ws = torch.empty(nb, dtype=torch.uint8, device=dev)
     _run(dev, "poetx_matmul_int8_grad", T, n, m, dz.data_ptr(), Wq.data_ptr(), wscale.data_ptr(), _DTYPE[dz.dtype],
@@ -224,7 +224,7 @@ def checkpoint_save(x: torch.Tensor) -> Checkpoint:
     T, d = _rows(x, "x")
     dev = x.device
     out = Checkpoint(torch.empty_like(x, dtype=torch.int8),
-                     torch.empty((T, (d + 31) // 32), dtype=torch.uint8, device=dev))
+                     torch.empty(T, (d + 31) // 32, dtype=torch.uint8, device=dev))
     _run(dev, "poetx_checkpoint_save", T, d, x.data_ptr(), _DTYPE[x.dtype], out.codes.data_ptr(),
          out.exps.data_ptr())
     return out
@@ -265,7 +265,7 @@ def block_backward(ckpt: Checkpoint, D: torch.Tensor, G: torch.Tensor, need_o: b
     if accumulate:
         _like(dG, "dG", torch.float32, G.shape, dev)
     else:
-        dG = torch.empty((d // b, b, b), dtype=torch.float32, device=dev)
+        dG = torch.empty(d // b, b, b, dtype=torch.float32, device=dev)
     O = torch.empty_like(D) if need_o else None
     dt = _DTYPE[D.dtype]
     nb = poetx_block_backward_workspace_bytes(T, d, b, dt)
