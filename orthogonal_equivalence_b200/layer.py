@@ -41,6 +41,20 @@ def _need(t, shape, dtype, device: torch.device, name: str) -> None:
         raise ValueError(f"{name}: must be contiguous")
 
 
+def _workspace(held: dict, kind: str, nbytes: int, device: torch.device) -> torch.Tensor:
+    """Scratch of a call: held and reused by eager calls (which are therefore
+    to be ordered on one stream), but a captured call's own, from its graph's
+    memory, so that no two graphs share it and no later eager call that needs
+    more can free it under a graph."""
+    if device.type == "cuda" and torch.cuda.is_current_stream_capturing():
+        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    ws = held.get(kind)
+    if ws is None or ws.numel() < nbytes:
+        ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+        held[kind] = ws
+    return ws
+
+
 class Saved(NamedTuple):
     """Activations the forward keeps for the backward: Y ([T][n], the P-side
     input in the Psi_P frame) and optionally Xg ([T][m], x in the Psi_R frame),
@@ -127,11 +141,7 @@ class PoetxLinear:
                           self.GR, self.GP, self.fold)
 
     def workspace(self, kind: str, nbytes: int) -> torch.Tensor:
-        ws = self._ws.get(kind)
-        if ws is None or ws.numel() < nbytes:
-            ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=self.device)
-            self._ws[kind] = ws
-        return ws
+        return _workspace(self._ws, kind, nbytes, self.device)
 
     # -------------------------------------------------------------- state
     def load(self, W0lin: torch.Tensor, permR: torch.Tensor, permP: torch.Tensor, qR: torch.Tensor,
@@ -388,8 +398,7 @@ class LayerGroup:
 
     def __init__(self, layers):
         self.layers = list(layers)
-        self._ws = None
-        self._bws = None
+        self._ws = {}
         self.q = None
         self.m1 = None
         self.m2 = None
@@ -451,13 +460,11 @@ class LayerGroup:
         _need(dG, (nblk, L0.b, L0.b), torch.float32, self.q.device, "dG")
         _need(dq, tuple(self.q.shape), torch.float32, self.q.device, "dq")
         nb = poetx_cnp_workspace_bytes(nblk, L0.b, L0.dtype)
-        if self._bws is None or self._bws.numel() < nb:
-            self._bws = torch.empty(max(nb, 1), dtype=torch.uint8, device=L0.device)
-        poetx_cnp_backward(nblk, L0.b, self.q, dG, dq, int(accumulate), L0.dtype, self._bws, nb, stream)
+        ws = _workspace(self._ws, "bwd", nb, L0.device)
+        poetx_cnp_backward(nblk, L0.b, self.q, dG, dq, int(accumulate), L0.dtype, ws, nb, stream)
 
     def build(self, stream=None) -> None:
         abis = [L._abi() for L in self.layers]
         nb = poetx_layers_cnp_workspace_bytes(abis)
-        if self._ws is None or self._ws.numel() < nb:
-            self._ws = torch.empty(max(nb, 1), dtype=torch.uint8, device=self.layers[0].device)
-        poetx_layers_cnp_build(abis, self._ws, nb, stream)
+        ws = _workspace(self._ws, "build", nb, self.layers[0].device)
+        poetx_layers_cnp_build(abis, ws, nb, stream)

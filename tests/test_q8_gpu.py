@@ -420,6 +420,59 @@ def test_empty_batches():
     assert O.shape == (0, 64) and not dG.any()
 
 
+# ---------------------------------------------------------------- offsets past 32 bits
+def test_rows_past_two_to_the_31():
+    # 150 001 rows of 14 336: 2.15e9 elements; the last rows against the same rows on their own
+    T, d = 150_001, 14_336
+    tail = rnd(70, 64, d, dtype=BF)
+    x = torch.zeros(T, d, dtype=BF, device="cuda")
+    x[-64:] = tail
+    gamma = rnd(71, d) + 1
+
+    def same(big, small):
+        for a, b in zip(big, small):
+            assert torch.equal(a[-64:], b)
+
+    q = px.quantize_rows(x)
+    same(q, px.quantize_rows(tail))
+    assert not q.scale[:-64].any() and torch.equal(px.dequantize_rows(q.codes, q.scale, BF)[-64:],
+                                                   px.dequantize_rows(q.codes[-64:].clone(), q.scale[-64:].clone(), BF))
+    del q
+    n, small = px.rmsnorm_quantize(x, gamma, x), px.rmsnorm_quantize(tail, gamma, tail)
+    same(n[:4], small[:4])
+    dx, dg = px.rmsnorm_backward(x, n.h, gamma, n.rstd)
+    dx1, dg1 = px.rmsnorm_backward(tail, small.h, gamma, small.rstd)
+    assert torch.equal(dx[-64:], dx1)
+    # the other rows add nothing; 64 terms in another order
+    assert ((dg - dg1).abs().double() <= 64 * U24 * (tail.double() * small.h.double() * small.rstd.double()[:, None]).abs().sum(0)).all()
+    del n, dx
+    c, c1 = px.checkpoint_save(x), px.checkpoint_save(tail)
+    same(c, c1)
+    assert torch.equal(px.checkpoint_load(c, BF)[-64:], px.checkpoint_load(c1, BF))
+    G = rnd(72, d // 256, 256, 256, dtype=BF, scale=0.1)
+    O, dG = px.block_backward(c, x, G)
+    O1, dG1 = px.block_backward(c1, tail, G)
+    assert torch.equal(O[-64:], O1) and not O[:-64].any()
+    X = px.checkpoint_load(c1, F32).double().view(64, -1, 256)
+    D = tail.double().view(64, -1, 256)
+    assert ((dG - dG1).abs().double() <= 4 * 98 * U24 * torch.einsum("tjr,tjc->jrc", X.abs(), D.abs())).all()
+
+
+@pytest.mark.parametrize("n", [14336, 14337])
+def test_products_past_two_to_the_31(n):
+    T, m = 150_001, 96
+    xq, xs, Wq, ws = codes(73, T, m), rnd(74, T).abs(), codes(75, n, m), rnd(76, n).abs()
+    z = px.matmul_int8(xq, xs, Wq, ws, BF)
+    for part in (slice(0, 300), slice(T // 2, T // 2 + 300), slice(T - 300, T)):
+        want = (xq[part].double() @ Wq.double().t()) * xs[part].double()[:, None] * ws.double()
+        within(z[part], want, (HALF[BF] + 3.1 * U24) * want.abs(), "z")
+    dx = px.matmul_int8_grad(z, Wq, ws)
+    part = slice(T - 300, T)
+    q, s = quantise64(z[part].float() * ws)
+    want = (q @ Wq.double()) * s.double()[:, None]
+    within(dx[part], want, (HALF[BF] + 2.1 * U24) * want.abs(), "dx")
+
+
 # ---------------------------------------------------------------- together
 def _chain_inputs(T, d, n):
     x, r = rnd(46, T, d, dtype=BF), rnd(47, T, d, dtype=BF)

@@ -209,6 +209,50 @@ def test_training_step_in_eight_bits():
     assert all(torch.equal(a, b) for a, b in zip(out, eager))
 
 
+def test_graphs_of_one_layer_hold_their_own_workspaces():
+    # two captured steps of one layer replayed on two streams at once, after an eager call that needed a
+    # larger workspace than either
+    L = layer(512, 768, 256, BF)
+    ins = [(rnd(30 + i, T, 512, dtype=BF), rnd(40 + i, T, 768, dtype=BF)) for i, T in enumerate((300, 200))]
+
+    def step(x, dz):
+        z, saved = L.forward(x, save_xg=True, save8=True)
+        return (z, *L.backward(None, saved, dz))
+
+    want = [step(*a) for a in ins]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for a in ins:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(step(*a))
+        graphs.append(g)
+    step(rnd(50, 900, 512, dtype=BF), rnd(51, 900, 768, dtype=BF))
+    junk = [torch.full((1 << 20,), float("nan"), device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(4):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(bool(torch.isnan(j).all()) for j in junk)
+    for o, w in zip(outs, want):
+        assert all(torch.equal(a, b) for a, b in zip(o, w))
+
+
+def test_empty_batch():
+    L = layer(256, 512, 256, BF)
+    x, dz = torch.empty(0, 256, dtype=BF, device="cuda"), torch.empty(0, 512, dtype=BF, device="cuda")
+    for _ in range(2):
+        z, kept = L.forward(x, save_xg=True, save8=True)
+        assert z.shape == (0, 512)
+        dx, dqR, dqP = L.backward(None, kept, dz)
+        assert dx.shape == (0, 256) and not dqR.any() and not dqP.any()
+        if not L.int8_product:
+            L.quantize_weight(int8_product=True)
+
+
 def test_refusals_of_the_layer():
     L = px.PoetxLinear(256, 256, 64, px.POETX_BF16, fold=px.POETX_FOLD_ALL)
     x = torch.zeros(4, 256, dtype=BF, device="cuda")
