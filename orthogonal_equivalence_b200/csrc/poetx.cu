@@ -1065,8 +1065,8 @@ poetx_status check_opt(const void* p) { return aligned16(p) ? POETX_OK : POETX_E
 // allows, K times eight elements a thread (more where the threads of a block
 // would not do); wider rows (K = 0) are read twice.  K trades the fixed work
 // of a row (reduction, scale: ~150 instructions a warp) against registers;
-// at 16384 x 4096 bf16, K = 1, 2, 4: rows to int8 50, 51, 45 us, norm 117, 90,
-// 90 us, its backward 92 (two blocks of 512 threads), 88, 150 us.
+// measured at 16384 x 4096 bf16 when it was chosen, K = 1, 2, 4: rows to int8
+// 50, 51, 45 us, norm 117, 90, 90 us, its backward 92, 88, 150 us.
 struct RowShape {
   int V, K, threads;
   bool full;
