@@ -2,7 +2,8 @@
 place, next to this file, with nvcc; `debug=True` builds libpoetx_debug.so,
 the same library compiled with -DPOETX_DEBUG (every TMA and bulk copy checked
 before it is issued; see csrc/ptx.cuh), loaded instead when the environment
-sets POETX_DEBUG=1."""
+sets POETX_DEBUG=1.  Either build also brings up to date _tensors.so, a Python
+extension (host code only) that calls whichever library is loaded."""
 from __future__ import annotations
 
 import glob
@@ -15,6 +16,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libpoetx.so")
 LIB_DEBUG = os.path.join(HERE, "libpoetx_debug.so")
+TENSORS = os.path.join(HERE, "_tensors.so")   # csrc/tensors.cpp: the torch side of quantized.py
 SOURCES = ["poetx.cu"]
 
 
@@ -37,7 +39,32 @@ def needs_build(lib: str = LIB) -> bool:
     return any(os.path.getmtime(d) > t for d in deps() if os.path.exists(d))
 
 
+def build_tensors(force: bool = False) -> str:
+    """The extension of csrc/tensors.cpp, compiled against the installed torch."""
+    src = [os.path.join(CSRC, "tensors.cpp"), os.path.join(ROOT, "include", "poetx.h")]
+    if not force and os.path.exists(TENSORS) and os.path.getmtime(TENSORS) >= max(os.path.getmtime(f) for f in src):
+        return TENSORS
+    import sysconfig
+
+    import torch
+    at = os.path.join(os.path.dirname(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
+    tmp = f"{TENSORS}.{os.getpid()}.tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(ROOT, "include"),
+           "-I", os.path.join(at, "include"), "-I", os.path.join(at, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"), src[0], "-o", tmp,
+           "-L", os.path.join(at, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError(f"{cmd[0]} failed building {os.path.basename(TENSORS)}")
+    os.replace(tmp, TENSORS)
+    return TENSORS
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
+    build_tensors(force)
     lib = LIB_DEBUG if debug else LIB
     if not force and not needs_build(lib):
         return lib
