@@ -35,7 +35,7 @@
 // with one per chunk and warp the kernel took 155 us instead of 120.
 //
 // 16384 x 4096 takes 87 us with the sum of the splits, 63 us without O (53 and
-// 32 us at the copy rate).  Neither HBM (41%) nor the tensor pipe (39%) is the
+// 32 us at the copy rate).  Neither HBM (48%) nor the tensor pipe (45%) is the
 // bound: a chunk's way from codes to MMA and back is, through the converting
 // warps (four of them: 96 us) and the rings' hand-overs; deeper rings of any of
 // the three operands change nothing.
