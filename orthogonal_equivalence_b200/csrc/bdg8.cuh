@@ -25,7 +25,7 @@
 //   warp 1: TMEM owner (both CTAs) and MMA issuer (leader only)
 //   warps 2-5: epilogues (both CTAs)
 //   warps 6-13: codes -> bf16 (both CTAs)
-//   warp 14: TMA producer of the codes (both CTAs)
+//   warp 14: producer of the codes and exponents (both CTAs)
 //
 // The arrivals at the leader's barriers that stand for shared-memory writes or
 // TMEM reads of this SM use the plain remote arrive: after the proxy fence (or
@@ -34,11 +34,17 @@
 // rest of the cluster.  A release at cluster scope waits for the memory system:
 // with one per chunk and warp the kernel took 155 us instead of 120.
 //
-// 16384 x 4096 takes 87 us with the sum of the splits, 63 us without O (53 and
-// 32 us at the copy rate).  Neither HBM (48%) nor the tensor pipe (45%) is the
-// bound: a chunk's way from codes to MMA and back is, through the converting
-// warps (four of them: 96 us) and the rings' hand-overs; deeper rings of any of
-// the three operands change nothing.
+// The exponents come to shared memory beside their codes, copied without a
+// register in between: loaded into registers, even a tile ahead, they held up
+// the converting warps (16384 x 4096 without O: 63 us instead of 54).  G_j is
+// released, and the next one loaded, before the last tile's dG; an item's first
+// O is computed while the dG before it is written.
+//
+// 16384 x 4096 takes 85 us with the sum of the splits (8 of them), 54 us without
+// O (53 and 32 us at the copy rate).  Neither HBM (48%) nor the tensor pipe (45%)
+// is the bound, nor the conversion (left out: 80 and 52 us; with four warps 9 us
+// more): the O tiles' way through registers and boxes and the ends of the items
+// are; deeper rings of any of the three operands change nothing.
 // Every wait is bounded (ptx.cuh).  No load uses multicast.
 #pragma once
 
@@ -63,7 +69,9 @@ constexpr int UNITS = 4;                        // ring of D units (TILE_BYTES e
 constexpr int XUNITS = 2;                       // converted X
 constexpr int SLOTS = 4;                        // codes
 constexpr int SLOT_BYTES = CH * HALF;           // 64 tokens x 128 codes
-constexpr int SMEM_BYTES = (UNITS + XUNITS) * TILE_BYTES + SLOTS * SLOT_BYTES + G_BYTES + EPI_BYTES + 1024 + 320;
+constexpr int EXP_BYTES = CH * 4;               // and their exponents, one word a token
+constexpr int SMEM_BYTES =
+    (UNITS + XUNITS) * TILE_BYTES + SLOTS * (SLOT_BYTES + EXP_BYTES) + G_BYTES + EPI_BYTES + 1024 + 320;
 constexpr int NUM_THREADS = 480;
 constexpr int CONV_WARPS = 8;
 constexpr int SPLIT_TOKENS = 2048;              // most tokens of a split (see above), about
@@ -119,6 +127,15 @@ __device__ __forceinline__ uint4 expand8(uint32_t w0, uint32_t w1, float s) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// Four bytes to shared memory without a register in between, zeros if !in.
+__device__ __forceinline__ void copy_word(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
+// An arrival at `bar` (of this CTA) once this thread's copies so far are in place.
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     bdg8_pair_kernel(const __grid_constant__ CUtensorMap tmDk, const __grid_constant__ CUtensorMap tmDmn,
                      const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmG,
@@ -132,7 +149,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   const uint32_t sG = sX + XUNITS * TILE_BYTES;
   const uint32_t sEpi = sG + G_BYTES;
   const uint32_t sCode = sEpi + EPI_BYTES;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + (sCode - smem_base) + SLOTS * SLOT_BYTES);
+  const uint32_t sExp = sCode + SLOTS * SLOT_BYTES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + (sExp - smem_base) + SLOTS * EXP_BYTES);
   // full[UNITS] (leader), empty[UNITS], xfull[XUNITS] (leader), xempty[XUNITS], cfull[SLOTS],
   // cempty[SLOTS], gfull (leader), gempty, ofull, oempty (leader), afull, aempty (leader)
   constexpr int FULL = 0, EMPTY = UNITS, XFULL = 2 * UNITS, XEMPTY = XFULL + XUNITS, CFULL = XEMPTY + XUNITS,
@@ -158,7 +176,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       mbar_init(bar(XEMPTY + s), 1);
     }
     for (int s = 0; s < SLOTS; ++s) {
-      mbar_init(bar(CFULL + s), 1);
+      mbar_init(bar(CFULL + s), 1 + 32);  // the codes' bytes, and each lane's exponents
       mbar_init(bar(CEMPTY + s), CONV_WARPS);
     }
     mbar_init(bar(GFULL), 1);
@@ -257,7 +275,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         int ta, tb;
         bdg2::split_tiles(p, s, ta, tb);
         if (p.want_o && !mbar_wait(bar(GFULL), local & 1, DERR_GEMM_WAIT)) { ok = false; break; }
-        if (!mbar_wait(bar(AEMPTY), (local & 1) ^ 1u, DERR_GEMM_WAIT)) { ok = false; break; }
         tc_fence_after();
         for (int tile = ta; tile < tb && ok; ++tile) {
           if (p.want_o) {
@@ -276,8 +293,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
             }
             if (!ok) break;
             tc2::commit_pair(bar(OFULL));
+            if (tile == tb - 1) tc2::commit_pair(bar(GEMPTY));  // G_j no longer read
             ++otiles;
           }
+          // the item before this one has left accG (its dG is written while this one's first O is computed)
+          if (tile == ta && !mbar_wait(bar(AEMPTY), (local & 1) ^ 1u, DERR_GEMM_WAIT)) { ok = false; break; }
           for (int c = 0; c < 4; ++c) {
             if (!mbar_wait(bar(FULL + unit), ring, DERR_GEMM_WAIT)) { ok = false; break; }
             if (!mbar_wait(bar(XFULL + xu), xring, DERR_GEMM_WAIT)) { ok = false; break; }
@@ -295,32 +315,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           }
         }
         if (!ok) break;
-        if (p.want_o) tc2::commit_pair(bar(GEMPTY));  // G_j no longer read
-        tc2::commit_pair(bar(AFULL));                  // also: every MMA of the item is done
+        tc2::commit_pair(bar(AFULL));  // every MMA of the item is done
       }
     }
   } else if (warp == 6 + CONV_WARPS) {
-    if (lane == 0) {
-      // ---------------- TMA producer of the codes (both CTAs)
-      prefetch_tmap(&tmX);
-      int slot = 0;
-      uint32_t ring = 0;
-      bool ok = true;
-      for (int item = pair; item < items && ok; item += npairs) {
-        int ta, tb;
-        bdg2::split_tiles(p, item / p.nblk, ta, tb);
-        const int fcol = (item % p.nblk) * BLK + int(rank) * HALF;
-        for (int chunk = ta * 4; chunk < tb * 4; ++chunk) {
-          if (!mbar_wait(bar(CEMPTY + slot), ring ^ 1u, DERR_GEMM_WAIT)) { ok = false; break; }
+    // ---------------- producer of the codes (TMA) and their exponents (both CTAs)
+    if (lane == 0) prefetch_tmap(&tmX);
+    int slot = 0;
+    uint32_t ring = 0;
+    bool ok = true;
+    for (int item = pair; item < items && ok; item += npairs) {
+      int ta, tb;
+      bdg2::split_tiles(p, item / p.nblk, ta, tb);
+      const int fcol = (item % p.nblk) * BLK + int(rank) * HALF;
+      for (int chunk = ta * 4; chunk < tb * 4; ++chunk) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(CEMPTY + slot), ring ^ 1u, DERR_GEMM_WAIT));
+        if (!ok) break;
+        if (lane == 0) {
           mbar_arrive_expect_tx(bar(CFULL + slot), SLOT_BYTES);
           tma_load_2d(sCode + slot * SLOT_BYTES, &tmX, bar(CFULL + slot), fcol, chunk * CH);
-          if (++slot == SLOTS) { slot = 0; ring ^= 1u; }
         }
+#pragma unroll
+        for (int r = lane; r < CH; r += 32) {
+          const int token = chunk * CH + r;  // behind the last one: exponent 0, which reads as 0 like the codes
+          const bool in = token < p.T;
+          copy_word(sExp + slot * EXP_BYTES + r * 4, pp.exps + int64_t(in ? token : 0) * pp.ng + fcol / q8::GROUP, in);
+        }
+        copies_arrive(bar(CFULL + slot));
+        if (++slot == SLOTS) { slot = 0; ring ^= 1u; }
       }
-      if (!ok) {
-        const uint64_t t0 = global_ns();
-        while (global_ns() - t0 < 100000ull) {
-        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (!ok && lane == 0) {
+      const uint64_t t0 = global_ns();
+      while (global_ns() - t0 < 100000ull) {
       }
     }
   } else if (warp >= 6) {
@@ -328,45 +356,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     const int ct = threadIdx.x - 192;
     const int row = ct & 63, group = ct >> 6;
     const uint32_t xfull_leader = tc2::map_to_rank(bar(XFULL), 0);
-    // The exponent of this thread's group in each chunk of a tile, loaded a
-    // tile ahead (rows behind the last token: 0, which reads as 0 like their
-    // codes).
-    uint32_t ex[4];
-    auto exponents_of = [&](int item) {  // of the item's block, first row of this thread
-      return pp.exps + ((item % p.nblk) * BLK + int(rank) * HALF) / q8::GROUP + group + int64_t(row) * pp.ng;
-    };
-    auto exponents = [&](const uint8_t* of, int token0, int c) {
-      ex[c] = token0 + c * CH + row < p.T
-                  ? __ldg(of + int64_t(token0 + c * CH) * pp.ng) : 0;
-    };
     int u = 0, slot = 0;
     uint32_t ring = 0, cring = 0;
     bool ok = true;
-    int ta, tb;
-    if (pair < items) {
-      bdg2::split_tiles(p, pair / p.nblk, ta, tb);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) exponents(exponents_of(pair), ta * BLK, c);
-    }
     for (int item = pair; item < items && ok; item += npairs) {
+      int ta, tb;
       bdg2::split_tiles(p, item / p.nblk, ta, tb);
-      const uint8_t* of = exponents_of(item);
       for (int tile = ta; tile < tb && ok; ++tile) {
-        int next0 = (tile + 1) * BLK;  // first token of the tile after this one
-        if (tile + 1 == tb) {
-          int first, last;
-          bdg2::split_tiles(p, (item + npairs) / p.nblk, first, last);
-          next0 = item + npairs < items ? first * BLK : p.T;
-          of = exponents_of(item + npairs);
-        }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           ok = ok && mbar_wait(bar(CFULL + slot), cring, DERR_GEMM_WAIT) &&
                mbar_wait(bar(XEMPTY + u), ring ^ 1u, DERR_GEMM_WAIT);
           ok = __all_sync(0xffffffffu, ok);
           if (ok) {
-            const float sc = q8::exponent_value(ex[c]);
-            exponents(of, next0, c);
+            uint32_t eb;
+            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(eb) : "r"(sExp + slot * EXP_BYTES + row * 4 + group) : "memory");
+            const float sc = q8::exponent_value(static_cast<uint8_t>(eb));
             const uint32_t src = sCode + slot * SLOT_BYTES + row * 128;
             const uint32_t dst = sX + u * TILE_BYTES + (group >> 1) * (CH * 128) + row * 128;
             const int d0 = (group & 1) * 4;  // this group's first 16-byte unit in the row of 64 columns
