@@ -1,11 +1,16 @@
 // Backward of one side of an fp32 layer from an 8-bit checkpoint of its
 // activation X (q8.cuh), both products of every block in one launch:
-//   O_j = D_j G_j^T              tiles of TS tokens x TS rows of G_j, over b
+//   O_j = D_j G_j^T              tiles of TM tokens x TS rows of G_j, over b
 //   part[s][j] = X_j^T D_j       tiles of TS x TS of dG_j, over the tokens of split s
-// FFMA throughout (the fp32 layer's arithmetic).  A block computes one tile:
-// 256 threads, (TS / 16)^2 sums each, KB terms staged in shared memory while
-// the next KB are loaded into registers; X is decoded as it is loaded.  Reads
-// of either operand run along its rows, whatever b is.
+// FFMA throughout (the fp32 layer's arithmetic).  A block computes one tile; a
+// thread holds 4 x 4 sums and reads four terms of either operand at once, two
+// 16-byte reads of shared memory for sixteen FFMA.  TS follows b (tile_of), so
+// that few of a tile's sums lie outside the block.  Where a TS x TS tile has
+// fewer sums than the block threads, groups of threads take every GR-th token
+// and are added up at the end, in order; O takes more tokens instead.  The next
+// KB terms are loaded into registers while the last ones are used; X is decoded
+// on its way to shared memory.  Rows of either operand are read along
+// themselves, 16 bytes a thread where b is a multiple of four (VEC).
 #pragma once
 
 #include <cstdint>
@@ -14,8 +19,6 @@
 
 namespace poetx {
 namespace bf32 {
-
-constexpr int KB = 32, THREADS = 256;
 
 struct Params {
   const float* D;       // [T][d]
@@ -30,104 +33,231 @@ struct Params {
   int64_t o_blocks;     // blocks that compute O (first in the grid)
 };
 
-// One tile: O (rows: tokens, columns: rows of G_j, K: columns of the block) or
-// dG (rows and columns of dG_j, K: tokens of the split).  `id` counts the tiles
-// of its kind.
-template <int TS, bool WANT_O>
-__device__ __forceinline__ void tile(const Params& p, int64_t id, float (*As)[TS + 1], float (*Bs)[TS + 1]) {
-  constexpr int R = TS / 16;             // sums per thread and dimension
-  constexpr int L = TS * KB / THREADS;   // loads per thread and operand
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+template <int TS>
+struct Shape {
+  static constexpr int C = TS / 4;                                       // threads along a side of the tile
+  static constexpr int GR = TS == 16 ? 16 : TS == 32 ? 4 : TS == 48 ? 2 : 1;  // groups over the tokens
+  static constexpr int NT = C * C * GR;                                  // 256, 256, 288, 256
+  static constexpr int TM = 4 * NT / C;                                  // tokens of an O tile: 256, 128, 96, 64
+  static constexpr int KBO = TS == 16 ? 16 : 32, KBG = TS == 16 ? 128 : TS == 32 ? 64 : 32;
+  static constexpr int LDM = TM + 4, LDS = TS + 4;                       // 16-byte rows, transposed stores without conflicts
+  static constexpr int WORDS_O = KBO * (LDM + LDS), WORDS_G = KBG * 2 * LDS, WORDS_R = GR > 1 ? GR * TS * TS : 0;
+  static constexpr int WORDS = WORDS_O > WORDS_G ? (WORDS_O > WORDS_R ? WORDS_O : WORDS_R)
+                                                 : (WORDS_G > WORDS_R ? WORDS_G : WORDS_R);
+};
+
+// Four elements from p on, those below `n`.
+template <bool VEC>
+__device__ __forceinline__ float4 load4(const float* p, int64_t n) {
+  float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (VEC) {
+    if (n > 0) r = *reinterpret_cast<const float4*>(p);
+  } else {
+    if (n > 0) r.x = p[0];
+    if (n > 1) r.y = p[1];
+    if (n > 2) r.z = p[2];
+    if (n > 3) r.w = p[3];
+  }
+  return r;
+}
+
+__device__ __forceinline__ void fma4x4(float (*acc)[4], const float4& u, const float4& v) {
+  const float a[4] = {u.x, u.y, u.z, u.w}, b[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[r][c] = fmaf(a[r], b[c], acc[r][c]);
+}
+
+// Rows 4 ty.. and columns 4 tx.. of a thread in a tile of C threads a row: a
+// warp covers 4 x 8 threads of the widest one (16 distinct words of either operand
+// would take a second pass).
+template <int C>
+__device__ __forceinline__ void place(int t, int& ty, int& tx) {
+  if (C == 16) {
+    tx = (t & 7) + 8 * (t >> 5 & 1);
+    ty = (t >> 3 & 3) + 4 * (t >> 6);
+  } else {
+    tx = t % C;
+    ty = t / C;
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void put_row(float* row, const float4& v, int n, int b) {
+  if (VEC) {
+    if (n < b) *reinterpret_cast<float4*>(row + n) = v;
+  } else {
+    if (n < b) row[n] = v.x;
+    if (n + 1 < b) row[n + 1] = v.y;
+    if (n + 2 < b) row[n + 2] = v.z;
+    if (n + 3 < b) row[n + 3] = v.w;
+  }
+}
+
+template <int TS, bool VEC>
+__device__ __forceinline__ void o_tile(const Params& p, int64_t id, float* sm) {
+  using S = Shape<TS>;
+  float* const As = sm;                    // [KBO][LDM]: D transposed
+  float* const Bs = sm + S::KBO * S::LDM;  // [KBO][LDS]: G_j transposed
   const int n0 = static_cast<int>(id % p.tiles_b) * TS;
   id /= p.tiles_b;
-  int64_t m0 = 0;
-  if constexpr (!WANT_O) {
-    m0 = id % p.tiles_b * TS;
-    id /= p.tiles_b;
-  }
   const int j = static_cast<int>(id % p.nblk), col = j * p.b;
-  const int64_t rest = id / p.nblk;      // token tile, or split
-  if constexpr (WANT_O) m0 = rest * TS;
-  const int64_t k_first = WANT_O ? 0 : rest * p.T / p.splits;
-  const int64_t k_last = WANT_O ? p.b : (rest + 1) * p.T / p.splits;
-  // this thread's elements: (tk + l * SK, ti + l * SI) of the stage
-  const int tk = WANT_O ? threadIdx.x % KB : threadIdx.x / TS;
-  const int ti = WANT_O ? threadIdx.x / KB : threadIdx.x % TS;
-  constexpr int SK = WANT_O ? 0 : THREADS / TS, SI = WANT_O ? THREADS / KB : 0;
-  float a[L], b[L];
-  auto fetch = [&](int64_t k0) {
-    const int64_t k = k0 + tk;
-    if constexpr (WANT_O) {
-      const float* d = p.D + (m0 + ti) * p.d + col + k;
-      const float* g = p.G + (static_cast<int64_t>(col) + n0 + ti) * p.b + k;
+  const int64_t m0 = id / p.nblk * S::TM;
+  constexpr int VA = S::TM * S::KBO / 4, VB = TS * S::KBO / 4;
+  constexpr int LA = (VA + S::NT - 1) / S::NT, LB = (VB + S::NT - 1) / S::NT;
+  // vector i of an operand: 32 lanes take two vectors of 16 rows, so that the
+  // four transposed stores of each meet 32 different banks
+  auto k_of = [](int i) { return (i >> 5) % (S::KBO / 8) * 8 + (i & 1) * 4; };
+  auto m_of = [](int i) { return (i >> 5) / (S::KBO / 8) * 16 + (i >> 1 & 15); };
+  float4 a[LA], b[LB];
+  auto fetch = [&](int k0) {
 #pragma unroll
-      for (int l = 0; l < L; ++l) {
-        a[l] = k < k_last && m0 + ti + l * SI < p.T ? d[static_cast<int64_t>(l * SI) * p.d] : 0.f;
-        b[l] = k < k_last && n0 + ti + l * SI < p.b ? g[static_cast<int64_t>(l * SI) * p.b] : 0.f;
-      }
-    } else {
-      const int ca = col + static_cast<int>(m0) + ti;
-      const bool ina = m0 + ti < p.b, inb = n0 + ti < p.b;
-      const int8_t* x = p.codes + k * p.d + ca;
-      const uint8_t* e = p.exps + k * p.ng + ca / q8::GROUP;
-      const float* d = p.D + k * p.d + col + n0 + ti;
-      int8_t q[L];
-      uint8_t eb[L];
+    for (int l = 0; l < LA; ++l) {
+      const int i = threadIdx.x + l * S::NT, k = k0 + k_of(i);
+      const int64_t m = m0 + m_of(i);
+      a[l] = load4<VEC>(p.D + m * p.d + col + k, (VA % S::NT == 0 || i < VA) && m < p.T ? p.b - k : 0);
+    }
 #pragma unroll
-      for (int l = 0; l < L; ++l) {
-        const bool in = k + l * SK < k_last;
-        q[l] = in && ina ? x[static_cast<int64_t>(l * SK) * p.d] : int8_t(0);
-        eb[l] = in && ina ? e[static_cast<int64_t>(l * SK) * p.ng] : uint8_t(0);
-        b[l] = in && inb ? d[static_cast<int64_t>(l * SK) * p.d] : 0.f;
-      }
-#pragma unroll
-      for (int l = 0; l < L; ++l) a[l] = static_cast<float>(q[l]) * q8::exponent_value(eb[l]);
+    for (int l = 0; l < LB; ++l) {
+      const int i = threadIdx.x + l * S::NT, k = k0 + k_of(i), n = n0 + m_of(i);
+      b[l] = load4<VEC>(p.G + (static_cast<int64_t>(col) + n) * p.b + k,
+                        (VB % S::NT == 0 || i < VB) && n < p.b ? p.b - k : 0);
     }
   };
-  float acc[R][R] = {};
-  fetch(k_first);
-  for (int64_t k0 = k_first; k0 < k_last; k0 += KB) {
+  auto stage = [&](float* to, int ld, int i, const float4& v) {
+    float* at = to + k_of(i) * ld + m_of(i);
+    at[0] = v.x;
+    at[ld] = v.y;
+    at[2 * ld] = v.z;
+    at[3 * ld] = v.w;
+  };
+  int ty, tx;
+  place<S::C>(threadIdx.x, ty, tx);
+  float acc[4][4] = {};
+  fetch(0);
+  for (int k0 = 0; k0 < p.b; k0 += S::KBO) {
 #pragma unroll
-    for (int l = 0; l < L; ++l) {
-      As[tk + l * SK][ti + l * SI] = a[l];
-      Bs[tk + l * SK][ti + l * SI] = b[l];
+    for (int l = 0; l < LA; ++l) {
+      const int i = threadIdx.x + l * S::NT;
+      if (VA % S::NT == 0 || i < VA) stage(As, S::LDM, i, a[l]);
+    }
+#pragma unroll
+    for (int l = 0; l < LB; ++l) {
+      const int i = threadIdx.x + l * S::NT;
+      if (VB % S::NT == 0 || i < VB) stage(Bs, S::LDS, i, b[l]);
     }
     __syncthreads();
-    if (k0 + KB < k_last) fetch(k0 + KB);
+    if (k0 + S::KBO < p.b) fetch(k0 + S::KBO);
 #pragma unroll 8
-    for (int k = 0; k < KB; ++k) {
-      float u[R], v[R];
+    for (int k = 0; k < S::KBO; ++k)
+      fma4x4(acc, *reinterpret_cast<const float4*>(As + k * S::LDM + 4 * ty),
+             *reinterpret_cast<const float4*>(Bs + k * S::LDS + 4 * tx));
+    __syncthreads();
+  }
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        u[r] = As[k][ty + 16 * r];
-        v[r] = Bs[k][tx + 16 * r];
+  for (int r = 0; r < 4; ++r) {
+    const int64_t m = m0 + 4 * ty + r;
+    if (m < p.T)
+      put_row<VEC>(p.O + m * p.d + col, make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]), n0 + 4 * tx, p.b);
+  }
+}
+
+template <int TS, bool VEC>
+__device__ __forceinline__ void dg_tile(const Params& p, int64_t id, float* sm) {
+  using S = Shape<TS>;
+  float* const As = sm;                    // [KBG][LDS]: X
+  float* const Bs = sm + S::KBG * S::LDS;  // [KBG][LDS]: D
+  const int n0 = static_cast<int>(id % p.tiles_b) * TS;
+  id /= p.tiles_b;
+  const int m0 = static_cast<int>(id % p.tiles_b) * TS;
+  id /= p.tiles_b;                         // split * nblk + j
+  const int j = static_cast<int>(id % p.nblk), col = j * p.b;
+  const int64_t s = id / p.nblk;
+  const int64_t k_first = s * p.T / p.splits, k_last = (s + 1) * p.T / p.splits;
+  constexpr int V = S::KBG * TS / 4, L = (V + S::NT - 1) / S::NT;
+  uint32_t q[L], eb[L];                    // four codes; their exponents
+  float4 b[L];
+  auto fetch = [&](int64_t k0) {
+#pragma unroll
+    for (int l = 0; l < L; ++l) {
+      const int i = threadIdx.x + l * S::NT, c = i % S::C * 4;
+      const int64_t k = k0 + i / S::C;
+      const bool in = (V % S::NT == 0 || i < V) && k < k_last;
+      b[l] = load4<VEC>(p.D + k * p.d + col + n0 + c, in ? p.b - n0 - c : 0);
+      const int left = in ? p.b - m0 - c : 0, at = col + m0 + c;
+      const int8_t* x = p.codes + k * p.d + at;
+      const uint8_t* e = p.exps + k * p.ng;
+      q[l] = eb[l] = 0;
+      if (VEC) {
+        if (left > 0) {
+          q[l] = *reinterpret_cast<const uint32_t*>(x);
+          eb[l] = e[at / q8::GROUP];
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+          if (h < left) {
+            q[l] |= static_cast<uint32_t>(static_cast<uint8_t>(x[h])) << 8 * h;
+            eb[l] |= static_cast<uint32_t>(e[(at + h) / q8::GROUP]) << 8 * h;
+          }
       }
+    }
+  };
+  auto decode = [](uint32_t w, uint32_t ew, int h) {
+    return static_cast<float>(static_cast<int8_t>(w >> 8 * h)) * q8::exponent_value(VEC ? ew : ew >> 8 * h & 0xffu);
+  };
+  const int g = threadIdx.x / (S::C * S::C);
+  int ty, tx;
+  place<S::C>(threadIdx.x % (S::C * S::C), ty, tx);
+  float acc[4][4] = {};
+  fetch(k_first);
+  for (int64_t k0 = k_first; k0 < k_last; k0 += S::KBG) {
 #pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int c = 0; c < R; ++c) acc[r][c] = fmaf(u[r], v[c], acc[r][c]);
+    for (int l = 0; l < L; ++l) {
+      const int i = threadIdx.x + l * S::NT, at = i / S::C * S::LDS + i % S::C * 4;
+      if (V % S::NT != 0 && i >= V) continue;
+      *reinterpret_cast<float4*>(As + at) =
+          make_float4(decode(q[l], eb[l], 0), decode(q[l], eb[l], 1), decode(q[l], eb[l], 2), decode(q[l], eb[l], 3));
+      *reinterpret_cast<float4*>(Bs + at) = b[l];
+    }
+    __syncthreads();
+    if (k0 + S::KBG < k_last) fetch(k0 + S::KBG);
+#pragma unroll 8
+    for (int k = 0; k < S::KBG / S::GR; ++k) {
+      const int row = (k * S::GR + g) * S::LDS;
+      fma4x4(acc, *reinterpret_cast<const float4*>(As + row + 4 * ty), *reinterpret_cast<const float4*>(Bs + row + 4 * tx));
     }
     __syncthreads();
   }
-  const int64_t rows = WANT_O ? p.T : p.b, ld = WANT_O ? p.d : p.b;
-  float* out = WANT_O ? p.O + col : p.part + id * p.b * static_cast<int64_t>(p.b);  // id = split * nblk + j
+  float* const out = p.part + id * p.b * static_cast<int64_t>(p.b);
+  if (S::GR == 1) {
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int64_t m = m0 + ty + 16 * r;
-    if (m >= rows) continue;
+    for (int r = 0; r < 4; ++r)
+      if (m0 + 4 * ty + r < p.b)
+        put_row<VEC>(out + static_cast<int64_t>(m0 + 4 * ty + r) * p.b,
+                     make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]), n0 + 4 * tx, p.b);
+  } else {
 #pragma unroll
-    for (int c = 0; c < R; ++c) {
-      const int n = n0 + tx + 16 * c;
-      if (n < p.b) out[m * ld + n] = acc[r][c];
+    for (int r = 0; r < 4; ++r)
+      *reinterpret_cast<float4*>(sm + (g * TS + 4 * ty + r) * TS + 4 * tx) =
+          make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
+    __syncthreads();
+    for (int i = threadIdx.x; i < TS * TS; i += S::NT) {
+      float v = sm[i];
+#pragma unroll
+      for (int h = 1; h < S::GR; ++h) v += sm[h * TS * TS + i];
+      const int m = m0 + i / TS, n = n0 + i % TS;
+      if (m < p.b && n < p.b) out[static_cast<int64_t>(m) * p.b + n] = v;
     }
   }
 }
 
-template <int TS>
-__global__ void __launch_bounds__(THREADS) block_backward_kernel(const Params p) {
-  __shared__ float As[KB][TS + 1], Bs[KB][TS + 1];
-  if (blockIdx.x < p.o_blocks) tile<TS, true>(p, blockIdx.x, As, Bs);
-  else tile<TS, false>(p, blockIdx.x - p.o_blocks, As, Bs);
+template <int TS, bool VEC>
+__global__ void __launch_bounds__(Shape<TS>::NT) block_backward_kernel(const Params p) {
+  __shared__ __align__(16) float sm[Shape<TS>::WORDS];
+  if (blockIdx.x < p.o_blocks) o_tile<TS, VEC>(p, blockIdx.x, sm);
+  else dg_tile<TS, VEC>(p, blockIdx.x - p.o_blocks, sm);
 }
 
 }  // namespace bf32

@@ -1424,9 +1424,13 @@ int bdg8_splits(int nblk, int64_t T) {
   return best;
 }
 
-// fp32: tiles of 32 where 64 would stand half empty; the tokens split until
-// six blocks a SM have work, with 64 tokens a split at least.
-int block_f32_tile(int b) { return b <= 32 ? 32 : 64; }
+// fp32: the tile (16, 32, 48 or 64) that covers b with the fewest sums outside
+// it; the tokens split until six blocks a SM have work, with 64 tokens a split
+// at least.
+int block_f32_tile(int b) {
+  if (b <= 32) return b <= 16 ? 16 : 32;
+  return (b + 47) / 48 * 48 < (b + 63) / 64 * 64 ? 48 : 64;
+}
 int block_f32_splits(int nblk, int b, int64_t T) {
   const int64_t tb = (b + block_f32_tile(b) - 1) / block_f32_tile(b);
   int64_t s = 6 * kSplitSMs / (nblk * tb * tb);
@@ -1456,12 +1460,19 @@ cudaError_t launch_block_f32(const void* D, const int8_t* codes, const uint8_t* 
   p.nblk = d / b;
   p.splits = splits;
   p.tiles_b = (b + ts - 1) / ts;
-  p.o_blocks = O ? (T + ts - 1) / ts * p.nblk * p.tiles_b : 0;
+  const int tm = ts == 16 ? bf32::Shape<16>::TM : ts == 32 ? bf32::Shape<32>::TM : ts == 48 ? bf32::Shape<48>::TM : bf32::Shape<64>::TM;
+  p.o_blocks = O ? (T + tm - 1) / tm * p.nblk * p.tiles_b : 0;
   const int64_t blocks = p.o_blocks + int64_t(splits) * p.nblk * p.tiles_b * p.tiles_b;
   if (blocks > 2147483647) return cudaErrorInvalidValue;
   const unsigned grid = static_cast<unsigned>(blocks);
-  if (ts == 32) bf32::block_backward_kernel<32><<<grid, bf32::THREADS, 0, st>>>(p);
-  else bf32::block_backward_kernel<64><<<grid, bf32::THREADS, 0, st>>>(p);
+#define POETX_F32_TILE(TS) \
+  if (ts == TS && b % 4 == 0) bf32::block_backward_kernel<TS, true><<<grid, bf32::Shape<TS>::NT, 0, st>>>(p); \
+  else if (ts == TS) bf32::block_backward_kernel<TS, false><<<grid, bf32::Shape<TS>::NT, 0, st>>>(p)
+  POETX_F32_TILE(16);
+  else POETX_F32_TILE(32);
+  else POETX_F32_TILE(48);
+  else POETX_F32_TILE(64);
+#undef POETX_F32_TILE
   return cudaGetLastError();
 }
 
