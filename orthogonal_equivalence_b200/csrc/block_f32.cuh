@@ -4,13 +4,17 @@
 //   part[s][j] = X_j^T D_j       tiles of TS x TS of dG_j, over the tokens of split s
 // FFMA throughout (the fp32 layer's arithmetic).  A block computes one tile; a
 // thread holds 4 x 4 sums and reads four terms of either operand at once, two
-// 16-byte reads of shared memory for sixteen FFMA.  TS follows b (tile_of), so
-// that few of a tile's sums lie outside the block.  Where a TS x TS tile has
-// fewer sums than the block threads, groups of threads take every GR-th token
-// and are added up at the end, in order; O takes more tokens instead.  The next
-// KB terms are loaded into registers while the last ones are used; X is decoded
-// on its way to shared memory.  Rows of either operand are read along
+// 16-byte reads of shared memory for eight packed FMA.  TS follows b, so that
+// few of a tile's sums lie outside the block.  Where a TS x TS tile has fewer
+// sums than the block threads, groups of threads take every GR-th token of the
+// stage and are added up at the end, in order; O takes more tokens instead.  The
+// next KB terms are loaded into registers while the last ones are used; X is
+// decoded on its way to shared memory.  Rows of either operand are read along
 // themselves, 16 bytes a thread where b is a multiple of four (VEC).
+//
+// 16384 x 2048, b = 64: 272 us, 16351 x 1920, b = 96: 454 us (123 and 172 us at
+// 70 TFLOP/s), bound by the shared reads.  8 x 8 sums a thread spill (O 17 us less
+// there, dG 20 us more, and 300 x 512 11.4 instead of 8.3 us).
 #pragma once
 
 #include <cstdint>
@@ -40,8 +44,9 @@ struct Shape {
   static constexpr int NT = C * C * GR;                                  // 256, 256, 288, 256
   static constexpr int TM = 4 * NT / C;                                  // tokens of an O tile: 256, 128, 96, 64
   static constexpr int KBO = TS == 16 ? 16 : 32, KBG = TS == 16 ? 128 : TS == 32 ? 64 : 32;
+  static constexpr int BLOCKS = TS == 64 ? 3 : 4;                        // a SM, by registers: 64 a thread; 80 for TS = 64
   static constexpr int LDM = TM + 4, LDS = TS + 4;                       // 16-byte rows, transposed stores without conflicts
-  static constexpr int WORDS_O = KBO * (LDM + LDS), WORDS_G = KBG * 2 * LDS, WORDS_R = GR > 1 ? GR * TS * TS : 0;
+  static constexpr int WORDS_O = KBO * (LDM + LDS), WORDS_G = KBG * 2 * LDS, WORDS_R = GR * TS * TS;
   static constexpr int WORDS = WORDS_O > WORDS_G ? (WORDS_O > WORDS_R ? WORDS_O : WORDS_R)
                                                  : (WORDS_G > WORDS_R ? WORDS_G : WORDS_R);
 };
@@ -61,17 +66,21 @@ __device__ __forceinline__ float4 load4(const float* p, int64_t n) {
   return r;
 }
 
-__device__ __forceinline__ void fma4x4(float (*acc)[4], const float4& u, const float4& v) {
-  const float a[4] = {u.x, u.y, u.z, u.w}, b[4] = {v.x, v.y, v.z, v.w};
+// acc += u v^T, two sums an instruction
+__device__ __forceinline__ void fma4x4(float (*acc)[4], const float* u, const float* v) {
+  const float4 x = *reinterpret_cast<const float4*>(u), y = *reinterpret_cast<const float4*>(v);
+  const float a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-  for (int r = 0; r < 4; ++r)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) acc[r][c] = fmaf(a[r], b[c], acc[r][c]);
+  for (int r = 0; r < 4; ++r) {
+    const float d[2] = {a[r], a[r]};
+    q8::fma2(acc[r], d, b);
+    q8::fma2(acc[r] + 2, d, b + 2);
+  }
 }
 
 // Rows 4 ty.. and columns 4 tx.. of a thread in a tile of C threads a row: a
-// warp covers 4 x 8 threads of the widest one (16 distinct words of either operand
-// would take a second pass).
+// warp covers 4 x 8 threads of the widest one, so that it reads few different
+// words of either operand.
 template <int C>
 __device__ __forceinline__ void place(int t, int& ty, int& tx) {
   if (C == 16) {
@@ -151,8 +160,7 @@ __device__ __forceinline__ void o_tile(const Params& p, int64_t id, float* sm) {
     if (k0 + S::KBO < p.b) fetch(k0 + S::KBO);
 #pragma unroll 8
     for (int k = 0; k < S::KBO; ++k)
-      fma4x4(acc, *reinterpret_cast<const float4*>(As + k * S::LDM + 4 * ty),
-             *reinterpret_cast<const float4*>(Bs + k * S::LDS + 4 * tx));
+      fma4x4(acc, As + k * S::LDM + 4 * ty, Bs + k * S::LDS + 4 * tx);
     __syncthreads();
   }
 #pragma unroll
@@ -181,8 +189,8 @@ __device__ __forceinline__ void dg_tile(const Params& p, int64_t id, float* sm) 
   auto fetch = [&](int64_t k0) {
 #pragma unroll
     for (int l = 0; l < L; ++l) {
-      const int i = threadIdx.x + l * S::NT, c = i % S::C * 4;
-      const int64_t k = k0 + i / S::C;
+      const int i = threadIdx.x + l * S::NT, c = i % (TS / 4) * 4;
+      const int64_t k = k0 + i / (TS / 4);
       const bool in = (V % S::NT == 0 || i < V) && k < k_last;
       b[l] = load4<VEC>(p.D + k * p.d + col + n0 + c, in ? p.b - n0 - c : 0);
       const int left = in ? p.b - m0 - c : 0, at = col + m0 + c;
@@ -215,7 +223,7 @@ __device__ __forceinline__ void dg_tile(const Params& p, int64_t id, float* sm) 
   for (int64_t k0 = k_first; k0 < k_last; k0 += S::KBG) {
 #pragma unroll
     for (int l = 0; l < L; ++l) {
-      const int i = threadIdx.x + l * S::NT, at = i / S::C * S::LDS + i % S::C * 4;
+      const int i = threadIdx.x + l * S::NT, at = i / (TS / 4) * S::LDS + i % (TS / 4) * 4;
       if (V % S::NT != 0 && i >= V) continue;
       *reinterpret_cast<float4*>(As + at) =
           make_float4(decode(q[l], eb[l], 0), decode(q[l], eb[l], 1), decode(q[l], eb[l], 2), decode(q[l], eb[l], 3));
@@ -226,35 +234,27 @@ __device__ __forceinline__ void dg_tile(const Params& p, int64_t id, float* sm) 
 #pragma unroll 8
     for (int k = 0; k < S::KBG / S::GR; ++k) {
       const int row = (k * S::GR + g) * S::LDS;
-      fma4x4(acc, *reinterpret_cast<const float4*>(As + row + 4 * ty), *reinterpret_cast<const float4*>(Bs + row + 4 * tx));
+      fma4x4(acc, As + row + 4 * ty, Bs + row + 4 * tx);
     }
     __syncthreads();
   }
   float* const out = p.part + id * p.b * static_cast<int64_t>(p.b);
-  if (S::GR == 1) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (m0 + 4 * ty + r < p.b)
-        put_row<VEC>(out + static_cast<int64_t>(m0 + 4 * ty + r) * p.b,
-                     make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]), n0 + 4 * tx, p.b);
-  } else {
+  for (int r = 0; r < 4; ++r)
+    *reinterpret_cast<float4*>(sm + (g * TS + 4 * ty + r) * TS + 4 * tx) =
+        make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
+  __syncthreads();
+  for (int i = threadIdx.x; i < TS * TS; i += S::NT) {
+    float v = sm[i];
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      *reinterpret_cast<float4*>(sm + (g * TS + 4 * ty + r) * TS + 4 * tx) =
-          make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
-    __syncthreads();
-    for (int i = threadIdx.x; i < TS * TS; i += S::NT) {
-      float v = sm[i];
-#pragma unroll
-      for (int h = 1; h < S::GR; ++h) v += sm[h * TS * TS + i];
-      const int m = m0 + i / TS, n = n0 + i % TS;
-      if (m < p.b && n < p.b) out[static_cast<int64_t>(m) * p.b + n] = v;
-    }
+    for (int h = 1; h < S::GR; ++h) v += sm[h * TS * TS + i];
+    const int m = m0 + i / TS, n = n0 + i % TS;
+    if (m < p.b && n < p.b) out[static_cast<int64_t>(m) * p.b + n] = v;
   }
 }
 
 template <int TS, bool VEC>
-__global__ void __launch_bounds__(Shape<TS>::NT) block_backward_kernel(const Params p) {
+__global__ void __launch_bounds__(Shape<TS>::NT, Shape<TS>::BLOCKS) block_backward_kernel(const Params p) {
   __shared__ __align__(16) float sm[Shape<TS>::WORDS];
   if (blockIdx.x < p.o_blocks) o_tile<TS, VEC>(p, blockIdx.x, sm);
   else dg_tile<TS, VEC>(p, blockIdx.x - p.o_blocks, sm);
