@@ -51,6 +51,57 @@ __device__ __forceinline__ void mma_one(uint32_t d_tmem, uint64_t a_desc, uint64
 // 32 integers of a TMEM row: the accumulators as loaded by tmem_ld_32cols.
 __device__ __forceinline__ int as_int(float v) { return __float_as_int(v); }
 
+// A block of 32 columns' scales from column c on (1 where there are none or no such column).
+__device__ __forceinline__ void load_scales(const float* bs, int c, int N, float* b) {
+  if (bs && c + 32 <= N) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const float4 f = __ldg(reinterpret_cast<const float4*>(bs + c) + q);
+      b[4 * q] = f.x;
+      b[4 * q + 1] = f.y;
+      b[4 * q + 2] = f.z;
+      b[4 * q + 3] = f.w;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) b[e] = bs && c + e < N ? __ldg(bs + c + e) : 1.f;
+  }
+}
+
+// A box (32 rows of 128 bytes, swizzled) to rows of N elements that start
+// anywhere, a word of the box a lane: bf16 rows on an odd element go out as the
+// pairs between their words, and the elements left over singly.
+template <typename T>
+__device__ __forceinline__ void store_box(uint32_t box, T* out, int64_t row0, int rows, int col0, int N, int lane) {
+  const int cols = min(static_cast<int>(128 / sizeof(T)), N - col0);
+  T* dst = out + row0 * N + col0;
+#pragma unroll 1
+  for (int r0 = 0; r0 < rows; r0 += 8) {
+    uint32_t w[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+      asm volatile("ld.shared.b32 %0, [%1];"
+                   : "=r"(w[r])
+                   : "r"(box + (r0 + r) * 128 + (((lane >> 2) ^ r) << 4) + (lane & 3) * 4)
+                   : "memory");
+#pragma unroll
+    for (int r = 0; r < 8; ++r, dst += N) {
+      if constexpr (sizeof(T) == 4) {
+        if (r0 + r < rows && lane < cols) dst[lane] = __uint_as_float(w[r]);
+      } else {
+        const int odd = (reinterpret_cast<uintptr_t>(dst) >> 1) & 1, c = 2 * lane + odd;
+        const uint32_t next = __shfl_down_sync(0xffffffffu, w[r], 1);
+        const uint32_t v = odd ? __funnelshift_r(w[r], next, 16) : w[r];
+        if (r0 + r < rows) {
+          if (c + 1 < cols) *reinterpret_cast<uint32_t*>(dst + c) = v;
+          if (c + 1 == cols) dst[c] = __ushort_as_bfloat16(static_cast<unsigned short>(v));
+          if (odd && lane == 0) dst[0] = __ushort_as_bfloat16(static_cast<unsigned short>(w[r]));
+        }
+      }
+    }
+  }
+}
+
 // ---------------------------------------------------------------- many tokens
 constexpr int STAGES = 6;
 constexpr int STAGE_BYTES = 2 * BOX_BYTES;  // this CTA's 128 tokens and 128 columns
@@ -198,6 +249,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       const uint32_t acc_phase = (local >> 1) & 1;
       const int row0 = mt * BM + rank * 128 + quarter * 32;
       const float as = row0 + lane < p.M ? pp.as[row0 + lane] : 0.f;
+      float b[32];  // scales of the next 32 columns, loaded while the ones before are at work
+      load_scales(pp.bs, nt * BN, p.N, b);
       bool ok = mbar_wait(bar(TFULL + acc), acc_phase, DERR_GEMM_WAIT);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
@@ -213,22 +266,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           float v[32];
           tmem_ld_32cols(tl + c0 + 32 * half, v);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const int c = col0 + 32 * half + 4 * q;
-            float b[4] = {1.f, 1.f, 1.f, 1.f};
-            if (pp.bs) {
-              if (c + 4 <= p.N) {
-                const float4 f = __ldg(reinterpret_cast<const float4*>(pp.bs + c));
-                b[0] = f.x; b[1] = f.y; b[2] = f.z; b[3] = f.w;
-              } else {
-#pragma unroll
-                for (int e = 0; e < 3; ++e)
-                  if (c + e < p.N) b[e] = __ldg(pp.bs + c + e);
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[4 * q + e] = static_cast<float>(as_int(v[4 * q + e])) * as * b[e];
-          }
+          for (int e = 0; e < 32; ++e) v[e] = static_cast<float>(as_int(v[e])) * as * b[e];
+          load_scales(pp.bs, col0 + 32 * half + 32, c0 + 32 * half + 32 < BN ? p.N : 0, b);
           if constexpr (sizeof(T) == 2) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) w[16 * half + i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
@@ -236,6 +275,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i]);
           }
+        }
+        if (c0 + CW == BN) {  // the accumulator is read
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc2::remote_arrive(tempty_leader + 8 * acc);
         }
         if (!rows_in || col0 >= p.N) continue;
         if (lane == 0) bulk_wait_read<1>();
@@ -257,22 +301,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           buf ^= 1;
         } else {
           __syncwarp();
-          T* out = static_cast<T*>(pp.out);
-          const uint8_t* bx = smem + (box - smem_base);
-          constexpr int PER = 16 / sizeof(T);
-          const int rows = min(32, p.M - row0);
-          for (int r = 0; r < rows; ++r)
-#pragma unroll
-            for (int c = lane; c < CW; c += 32)
-              if (col0 + c < p.N)
-                out[static_cast<int64_t>(row0 + r) * p.N + col0 + c] =
-                    reinterpret_cast<const T*>(bx + r * 128 + (((c / PER) ^ (r & 7)) << 4))[c % PER];
+          store_box<T>(box, static_cast<T*>(pp.out), row0, min(32, p.M - row0), col0, p.N, lane);
           __syncwarp();
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tc2::remote_arrive(tempty_leader + 8 * acc);
     }
     if (lane == 0) bulk_wait_all();
   }
