@@ -106,9 +106,10 @@ __device__ __forceinline__ void store_box(uint32_t box, T* out, int64_t row0, in
 constexpr int STAGES = 6;
 constexpr int STAGE_BYTES = 2 * BOX_BYTES;  // this CTA's 128 tokens and 128 columns
 constexpr int EPI_BOX = 32 * 128;
-constexpr int EPI_BYTES = 4 * 2 * EPI_BOX;
+constexpr int EPI_WARPS = 8;                // two a quarter of the rows, half the columns each
+constexpr int EPI_BYTES = EPI_WARPS * EPI_BOX;
 constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_BYTES + 1024 + 256;
-constexpr int NUM_THREADS = 192;
+constexpr int PAIR_THREADS = 64 + 32 * EPI_WARPS;
 
 struct PairParams {
   tc2::Params g;        // sizes, raster, instruction descriptor
@@ -127,7 +128,7 @@ struct PairParams {
 // gradient's product 8192 x 14336 -> 4096 294 us (91%).  Asking L2 for operands
 // ahead of the stages costs 10% (the way from L2 to the SMs is nearly full too).
 template <typename T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
     product_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                         const __grid_constant__ CUtensorMap tmC, const PairParams pp) {
   extern __shared__ uint8_t smem_raw[];
@@ -153,7 +154,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(bar(TFULL + a), 1);
-      mbar_init(bar(TEMPTY + a), 8);  // 4 epilogue warps x 2 CTAs
+      mbar_init(bar(TEMPTY + a), 2 * EPI_WARPS);  // of both CTAs
     }
     mbar_init(bar(DRAIN), 1);
     fence_barrier_init();
@@ -237,10 +238,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   } else {
     // ---------------- epilogue (both CTAs): this CTA's 128 rows of each tile
     constexpr int CW = 128 / sizeof(T);  // columns of a box
-    const int quarter = warp & 3;
-    const uint32_t my_boxes = sEpi + (warp - 2) * 2 * EPI_BOX;
+    const int quarter = warp & 3, first = (warp - 2) / 4 * (BN / 2);  // rows, and columns of the tile
+    const uint32_t box = sEpi + (warp - 2) * EPI_BOX;
     const uint32_t tempty_leader = tc2::map_to_rank(bar(TEMPTY), 0);
-    int buf = 0;
+    // the scales of a tile's rows and of the next 32 columns are loaded ahead
+    auto token_scale = [&](int tile) {
+      int mt, nt;
+      tc2::decode(p, tile, mt, nt);
+      const int row = mt * BM + static_cast<int>(rank) * 128 + quarter * 32 + lane;
+      return row < p.M ? __ldg(pp.as + row) : 0.f;
+    };
+    auto first_col = [&](int tile) {
+      int mt, nt;
+      tc2::decode(p, tile, mt, nt);
+      return nt * BN + first;
+    };
+    float as_next = 0.f, b[32];
+    if (pair < total) {
+      as_next = token_scale(pair);
+      load_scales(pp.bs, first_col(pair), p.N, b);
+    }
     int local = 0;
     for (int tile = pair; tile < total; tile += npairs, ++local) {
       int mt, nt;
@@ -248,9 +265,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       const int acc = local & 1;
       const uint32_t acc_phase = (local >> 1) & 1;
       const int row0 = mt * BM + rank * 128 + quarter * 32;
-      const float as = row0 + lane < p.M ? pp.as[row0 + lane] : 0.f;
-      float b[32];  // scales of the next 32 columns, loaded while the ones before are at work
-      load_scales(pp.bs, nt * BN, p.N, b);
+      const float as = as_next;
+      const int next = tile + npairs;
+      if (next < total) as_next = token_scale(next);
+      const int next_col = next < total ? first_col(next) : p.N;
       bool ok = mbar_wait(bar(TFULL + acc), acc_phase, DERR_GEMM_WAIT);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
@@ -258,7 +276,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       const bool rows_in = row0 < p.M;
       const uint32_t tl = tmem_base + acc * BN + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll 1
-      for (int c0 = 0; c0 < BN; c0 += CW) {
+      for (int c0 = first; c0 < first + BN / 2; c0 += CW) {
         const int col0 = nt * BN + c0;
         uint32_t w[32];
 #pragma unroll
@@ -267,7 +285,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           tmem_ld_32cols(tl + c0 + 32 * half, v);
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] = static_cast<float>(as_int(v[e])) * as * b[e];
-          load_scales(pp.bs, col0 + 32 * half + 32, c0 + 32 * half + 32 < BN ? p.N : 0, b);
+          load_scales(pp.bs, c0 + 32 * half + 32 < first + BN / 2 ? col0 + 32 * half + 32 : next_col, p.N, b);
           if constexpr (sizeof(T) == 2) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) w[16 * half + i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
@@ -276,15 +294,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
             for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i]);
           }
         }
-        if (c0 + CW == BN) {  // the accumulator is read
+        if (c0 + CW == first + BN / 2) {  // this warp's part of the accumulator is read
           tc_fence_before();
           __syncwarp();
           if (lane == 0) tc2::remote_arrive(tempty_leader + 8 * acc);
         }
         if (!rows_in || col0 >= p.N) continue;
-        if (lane == 0) bulk_wait_read<1>();
+        if (lane == 0) bulk_wait_read<0>();
         __syncwarp();
-        const uint32_t box = my_boxes + buf * EPI_BOX;
         const uint32_t rowp = box + lane * 128;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
@@ -298,7 +315,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
             tma_store_2d(&tmC, box, col0, row0);
             bulk_commit();
           }
-          buf ^= 1;
         } else {
           __syncwarp();
           store_box<T>(box, static_cast<T*>(pp.out), row0, min(32, p.M - row0), col0, p.N, lane);
@@ -321,6 +337,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 }
 
 // ---------------------------------------------------------------- few tokens
+constexpr int NUM_THREADS = 192;
+
 struct WideParams {
   const float* as;      // [T] token scales
   const float* bs;      // [N] scales of the weight's side or NULL

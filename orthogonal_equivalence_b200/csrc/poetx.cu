@@ -1332,7 +1332,7 @@ cudaError_t launch_pair_i8(const ProductI8& q, cudaStream_t st, int device) {
   pp.out = q.out;
   const int tiles = p.tiles_m * p.tiles_n;
   const int pairs = sm_count(device) / 2;
-  i8::product_pair_kernel<T><<<2 * (tiles < pairs ? tiles : pairs), i8::NUM_THREADS, i8::SMEM_BYTES, st>>>(ma, mb, mc,
+  i8::product_pair_kernel<T><<<2 * (tiles < pairs ? tiles : pairs), i8::PAIR_THREADS, i8::SMEM_BYTES, st>>>(ma, mb, mc,
                                                                                                          pp);
   return cudaGetLastError();
 }
