@@ -1339,12 +1339,14 @@ cudaError_t launch_pair_i8(const ProductI8& q, cudaStream_t st, int device) {
 
 // Tiles of the wide kernel, or nt = 0 where the pair kernel is the faster one.
 // Up to 64 tokens take the narrowest tile that holds them.  Beyond, a tile of
-// 64 tokens as long as two CTAs a SM hold them all, then one of 128, then the
-// pair kernel; in us (64, 128, pair), product of T tokens by [n][m]:
-//   333 x 4096 -> 1024:  9.7, 10.5, 24   512 x 4096 -> 4096:  17, 18, 26
-//   1024 x 4096 -> 4096: 28, 23, 26      256 x 4096 -> 14336: 27, 24, 28
-//   512 x 4096 -> 14336: 50, 44, 40      1111 x 5120 -> 13824: 118, 99, 68
-// A long K (512 x 14336 -> 4096: 41, 35) pays for 128 sooner, split in two.
+// 64 tokens as long as two CTAs a SM hold them all (128 up to 128 tokens, half of
+// a pair's tile), then the pair kernel; in us (64, 128, pair), product of T
+// tokens by [n][m]:
+//   333 x 4096 -> 1024:  8.4, 8.7, 16.5   512 x 4096 -> 4096:   15.9, 16.2, 17.0
+//   4096 x 512 -> 512:   7.1, 9.2, 8.7    2048 x 4096 -> 1024:  15.5, 16.3, 16.7
+//   256 x 4096 -> 14336: 30, 21.8, 18.0   1024 x 4096 -> 4096:  30, 21.5, 17.7
+//   2048 x 512 -> 2048:  13.2, 10.0, 8.9  10218 x 512 -> 192:   11.9, 9.7, 8.0
+// A long K (512 x 14336 -> 4096: 40, 33.5, 41) pays for 128 sooner, split in two.
 // K is split over 2, 4 or 8 CTAs while they all stay resident, four narrow
 // CTAs a SM, else two (200 x 4096 -> 4096: 15.9 us whole, 13.4 in two); 3, 5
 // or 6 fit the GPCs badly (1 x 4096 -> 14336: 12.7 us for four, 15 for five).
@@ -1355,7 +1357,7 @@ WideShape wide_shape(int T, int N, int K, int device) {
   const int nkb = (K + i8::KB - 1) / i8::KB;
   if (T <= 64) w.nt = T <= 16 ? 16 : T <= 32 ? 32 : 64;
   else if (tiles_of(64) <= 2 * sms) w.nt = nkb >= 64 && tiles_of(64) > sms && tiles_of(128) <= sms ? 128 : 64;
-  else if (T <= 128 || tiles_of(128) <= 2 * sms) w.nt = 128;
+  else if (T <= 128) w.nt = 128;
   else return w;
   const int64_t tiles = tiles_of(w.nt);
   const int most = w.nt <= 32 ? 4 : 2;  // CTAs a SM holds
