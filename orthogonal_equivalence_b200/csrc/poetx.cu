@@ -1062,30 +1062,48 @@ poetx_status check_rows(int64_t T, int32_t d, int32_t max_d) {
 poetx_status check_opt(const void* p) { return aligned16(p) ? POETX_OK : POETX_E_ALIGN; }
 
 // Threads and registers of a row: 16-byte vectors (V = 8) where the row length
-// allows, K times eight elements a thread (more where the threads of a block
-// would not do); wider rows (K = 0) are read twice.  K trades the fixed work
-// of a row (reduction, scale: ~150 instructions a warp) against registers;
-// measured at 16384 x 4096 bf16 when it was chosen, K = 1, 2, 4: rows to int8
-// 50, 51, 45 us, norm 117, 90, 90 us, its backward 92, 88, 150 us.
+// is a multiple of eight, the array's own 16-byte units (V = 2) where it is not
+// and lies between `shifted` and the width whose gain fits shared memory twice,
+// else single elements (V = 1).  In us, V = 2 and V = 1, bf16: rows to int8 16384
+// x 405 28, 17, x 810 25, 32, x 2261 68, 83, 4999 x 8001 50, 184; norm backward
+// 16384 x 810 39, 38, x 1310 65, 83, 4999 x 8001 92, 556, in fp32 6153 x 6500 146,
+// 123, 4999 x 8001 160, 210.
+// A thread takes K times eight elements (more where the threads of a block would
+// not do); wider rows (K = 0) are read twice.  K trades the fixed work of a row
+// (reduction, scale: ~150 instructions a warp) against registers; measured at
+// 16384 x 4096 bf16 when it was chosen, K = 1, 2, 4: rows to int8 50, 51, 45 us,
+// norm 117, 90, 90 us, its backward 92, 88, 150 us.
+constexpr int kMaxShifted = 24576;
 struct RowShape {
   int V, K, threads;
   bool full;
 };
-RowShape row_shape(int d, int k) {
+RowShape row_shape(int d, int k, int shifted) {
   RowShape r;
-  r.V = d % 8 == 0 ? 8 : 1;
+  r.V = d % 8 == 0 ? 8 : d >= shifted && d <= kMaxShifted ? 2 : 1;
   if (r.V == 1 && k > 1) k /= 2;
-  while (k < 4 && d > k * 8 * q8::kRowThreads) k *= 2;
-  r.K = d <= k * 8 * q8::kRowThreads ? k : 0;
-  const int t = ((d + 8 * k - 1) / (8 * k) + 31) / 32 * 32;
+  const int n = r.V == 2 ? d + 7 : d;  // with the elements that share the row's first unit
+  while (k < 4 && n > k * 8 * q8::kRowThreads) k *= 2;
+  r.K = n <= k * 8 * q8::kRowThreads ? k : 0;
+  const int t = ((n + 8 * k - 1) / (8 * k) + 31) / 32 * 32;
   r.threads = t < q8::kRowThreads ? t : q8::kRowThreads;
   r.full = r.K > 0 && r.V == 8 && d == r.threads * 8 * r.K;
   return r;
 }
-RowShape quantize_shape(int d, int32_t dtype) { return row_shape(d, dtype == POETX_BF16 ? 4 : 2); }
-RowShape norm_shape(int d, int32_t dtype) { return row_shape(d, dtype == POETX_BF16 ? 2 : 1); }
+// Shared memory for a row's gain (V = 2).
+size_t gain_bytes(const RowShape& r, int d) {
+  if (r.V != 2) return 0;
+  return sizeof(float) * size_t(r.K > 0 ? r.K * r.threads * 8 : (d + 14) / 8 * 8);
+}
+// Blocks of a grid of rows: V = 2 wants a multiple of eight (or a row a block).
+int64_t row_grid(const RowShape& r, int64_t T, int64_t g) {
+  if (r.V == 2) g = g / 8 * 8;
+  return T < g ? T : g;
+}
+RowShape quantize_shape(int d, int32_t dtype) { return row_shape(d, dtype == POETX_BF16 ? 4 : 2, 640); }
+RowShape norm_shape(int d, int32_t dtype) { return row_shape(d, dtype == POETX_BF16 ? 2 : 1, 640); }
 RowShape norm_grad_shape(int d, int32_t dtype) {
-  RowShape r = row_shape(d, dtype == POETX_BF16 ? 2 : 1);
+  RowShape r = row_shape(d, dtype == POETX_BF16 ? 2 : 1, dtype == POETX_BF16 ? 1024 : 7169);
   if (dtype == POETX_FP32 && r.K == 4) {  // four times eight fp32 elements of three arrays do not fit the registers
     r.K = 0;
     r.full = false;
@@ -1107,6 +1125,10 @@ cudaError_t with_shape(const RowShape& r, F f) {
   POETX_SHAPE(8, 2, false);
   POETX_SHAPE(8, 4, false);
   POETX_SHAPE(8, 0, false);
+  POETX_SHAPE(2, 1, false);
+  POETX_SHAPE(2, 2, false);
+  POETX_SHAPE(2, 4, false);
+  POETX_SHAPE(2, 0, false);
   POETX_SHAPE(1, 1, false);
   POETX_SHAPE(1, 2, false);
   POETX_SHAPE(1, 4, false);
@@ -1139,8 +1161,13 @@ cudaError_t launch_rows(const q8::RowsParams& p, cudaStream_t st, int device) {
     int per_sm;
     const cudaError_t e = blocks_per_sm(kernel, r.threads, &regs[device & 63], &per_sm);
     if (e != cudaSuccess) return e;
-    const int64_t g = int64_t(sm_count(device)) * per_sm;
-    kernel<<<static_cast<int>(p.T < g ? p.T : g), r.threads, 0, st>>>(p);
+    const size_t smem = p.gain ? gain_bytes(r, p.d) : 0;
+    static bool attr[64] = {false};
+    const cudaError_t ea = allow_smem(kernel, smem, &attr[device & 63]);
+    if (ea != cudaSuccess) return ea;
+    const int by_smem = static_cast<int>(220 * 1024 / (smem + 2048));
+    const int64_t g = int64_t(sm_count(device)) * (by_smem < per_sm ? by_smem : per_sm);
+    kernel<<<static_cast<int>(row_grid(r, p.T, g)), r.threads, smem, st>>>(p);
     return cudaGetLastError();
   });
 }
@@ -1167,17 +1194,16 @@ cudaError_t quantize_rows(int64_t T, int32_t d, const void* x, int32_t dtype, co
 
 // Blocks of the norm's backward: a fixed number, so that the sums of dgamma
 // do not depend on the device.
-int norm_grad_grid(int64_t T, int threads) {
-  const int per_sm = 512 / threads;
-  const int64_t g = int64_t(kSplitSMs) * (per_sm < 1 ? 1 : per_sm > 16 ? 16 : per_sm);
-  return static_cast<int>(T < g ? T : g);
+int norm_grad_grid(int64_t T, const RowShape& r) {
+  const int per_sm = 512 / r.threads;
+  return static_cast<int>(row_grid(r, T, int64_t(kSplitSMs) * (per_sm < 1 ? 1 : per_sm > 16 ? 16 : per_sm)));
 }
 
 template <typename T>
 cudaError_t launch_norm_grad(const q8::NormGradParams& p, int grid, const RowShape& r, cudaStream_t st, int device) {
   return with_shape(r, [&](auto V, auto K, auto FULL) {
     auto kernel = q8::norm_grad_kernel<T, decltype(V)::value, decltype(K)::value, decltype(FULL)::value>;
-    const size_t smem = K > 0 ? 0 : sizeof(float) * size_t(p.d);
+    const size_t smem = gain_bytes(r, p.d) + (K > 0 ? 0 : sizeof(float) * size_t(r.V == 2 ? (p.d + 14) / 8 * 8 : p.d));
     static bool attr[64] = {false};
     const cudaError_t e = allow_smem(kernel, smem, &attr[device & 63]);
     if (e != cudaSuccess) return e;
@@ -2524,7 +2550,7 @@ poetx_status poetx_rmsnorm_quantize(int64_t T, int32_t d, const void* x, const v
 
 size_t poetx_rmsnorm_backward_workspace_bytes(int64_t T, int32_t d, int32_t dtype) {
   if (check_dtype(dtype) != POETX_OK || check_rows(T, d, kMaxM) != POETX_OK) return 0;
-  return kAlign + al(sizeof(float) * size_t(norm_grad_grid(T, norm_grad_shape(d, dtype).threads)) * d);
+  return kAlign + al(sizeof(float) * size_t(norm_grad_grid(T, norm_grad_shape(d, dtype))) * d);
 }
 
 poetx_status poetx_rmsnorm_backward(int64_t T, int32_t d, const void* dy, const void* h, const float* gamma,
@@ -2545,7 +2571,7 @@ poetx_status poetx_rmsnorm_backward(int64_t T, int32_t d, const void* dy, const 
   int dev;
   POETX_TRY(current_device(&dev));
   const RowShape r = norm_grad_shape(d, dtype);
-  const int grid = norm_grad_grid(T, r.threads);
+  const int grid = norm_grad_grid(T, r);
   Carver c(ws, ws_bytes);
   q8::NormGradParams p;
   p.dy = dy;

@@ -28,9 +28,13 @@ constexpr int kRowThreads = 448;   // most threads of a row's block: two blocks 
 
 // ---------------------------------------------------------------- loads and stores
 // Eight elements of a row of d as loaded: consecutive ones from c (V = 8,
-// whole 16-byte vectors), or c, c + nt, ... (V = 1, any row).  Behind the
-// row's end: zeros.  FULL: the block's threads cover the row exactly, nothing
-// to check.
+// whole 16-byte vectors), or c, c + nt, ... (V = 1, any row).  Outside the
+// row: zeros.  FULL: the block's threads cover the row exactly, nothing to
+// check.  V = 2: rows of a d that is no multiple of eight, taken by the array's
+// own 16-byte units: a row that starts `phase` elements behind one has c =
+// -phase, 8 - phase, ..., and the units it shares with its neighbours are
+// loaded and stored one element at a time.  The phase, (row * d) % 8, is the same
+// for all rows of a block, since the grid is a multiple of eight.
 template <typename T, int V>
 struct Raw8 {
   T v[8];
@@ -43,12 +47,40 @@ template <>
 struct Raw8<float, 8> {
   float4 v[2];
 };
+template <>
+struct Raw8<__nv_bfloat16, 2> : Raw8<__nv_bfloat16, 8> {
+  __device__ __forceinline__ void from(const __nv_bfloat16* e) {
+    auto two = [&](int i) {
+      return static_cast<uint32_t>(__bfloat16_as_ushort(e[i])) | static_cast<uint32_t>(__bfloat16_as_ushort(e[i + 1])) << 16;
+    };
+    v = make_uint4(two(0), two(2), two(4), two(6));
+  }
+};
+template <>
+struct Raw8<float, 2> : Raw8<float, 8> {
+  __device__ __forceinline__ void from(const float* e) {
+    v[0] = make_float4(e[0], e[1], e[2], e[3]);
+    v[1] = make_float4(e[4], e[5], e[6], e[7]);
+  }
+};
+
+// Is the unit at c all inside the row?
+__device__ __forceinline__ bool inside8(int c, int d) { return c >= 0 && c + 8 <= d; }
 
 template <typename T, int V, bool FULL>
 __device__ __forceinline__ void fetch8(Raw8<T, V>& r, const T* p, int c, int nt, int d) {
   if constexpr (V == 1) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) r.v[e] = c + e * nt < d ? p[c + e * nt] : from_f32<T>(0.f);
+  } else if constexpr (V == 2) {
+    if (inside8(c, d)) {
+      fetch8<T, 8, true>(r, p, c, nt, d);
+    } else {
+      T v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = c + e >= 0 && c + e < d ? p[c + e] : from_f32<T>(0.f);
+      r.from(v);
+    }
   } else if constexpr (std::is_same<T, float>::value) {
     const bool in = FULL || c < d;
     r.v[0] = in ? reinterpret_cast<const float4*>(p + c)[0] : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -103,6 +135,12 @@ __device__ __forceinline__ void put8(T* p, int c, int nt, int d, const Raw8<T, V
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       if (c + e * nt < d) p[c + e * nt] = r.v[e];
+  } else if (V == 2 && !inside8(c, d)) {
+    float f[8];
+    unpack8<T, V>(r, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c + e >= 0 && c + e < d) p[c + e] = from_f32<T>(f[e]);
   } else if (FULL || c < d) {
     if constexpr (std::is_same<T, float>::value) {
       reinterpret_cast<float4*>(p + c)[0] = r.v[0];
@@ -123,6 +161,17 @@ __device__ __forceinline__ void store8(T* p, int c, int nt, int d, const float* 
   Raw8<T, V> r;
   pack8<T, V>(r, f);
   put8<T, V, FULL>(p, c, nt, d, r);
+}
+
+// V = 2: `n` floats of a row's gain (zeros outside it) as the units see them, in
+// shared memory.
+__device__ __forceinline__ void stage_gain(float* sm, const float* gain, int phase, int n, int d) {
+  for (int i = threadIdx.x; i < n; i += blockDim.x) sm[i] = i >= phase && i - phase < d ? gain[i - phase] : 0.f;
+}
+template <int V, bool FULL>
+__device__ __forceinline__ void load_gain(const float* gain, const float* sm, int phase, int c, int nt, int d, float* g) {
+  if constexpr (V == 2) load8<float, 8, true>(sm, c + phase, nt, d, g);
+  else load8<float, V, FULL>(gain, c, nt, d, g);
 }
 
 // ---------------------------------------------------------------- two values an instruction
@@ -196,8 +245,12 @@ __device__ __forceinline__ uint32_t quantise_border(float u, const RowScale& r) 
 // The codes of eight values (placed as in load8).  The quotient lies between
 // u * lo and u * hi; where both round to the same integer that is the code
 // (two FMAs a value, one branch for all eight).
-template <int V, bool FULL>
-__device__ __forceinline__ void store_codes(int8_t* p, int c, int nt, int d, const float* u, const RowScale& r) {
+// V = 2: where the codes' rows lie like the values' (like), a unit is eight
+// bytes on a boundary; rows that start on a boundary of their own take theirs
+// from two neighbouring lanes (WARP: all lanes call).
+template <int V, bool FULL, bool WARP>
+__device__ __forceinline__ void store_codes(int8_t* p, int c, int nt, int d, const float* u, const RowScale& r,
+                                            bool like, int phase) {
   uint32_t q[8];
   if (r.kind == 1) {
     uint32_t differ = 0;
@@ -220,11 +273,33 @@ __device__ __forceinline__ void store_codes(int8_t* p, int c, int nt, int d, con
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (c + i * nt < d) p[c + i * nt] = static_cast<int8_t>(q[i]);
-  } else if (FULL || c < d) {
+  } else {
     uint2 w;
     w.x = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
     w.y = __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410);
-    *reinterpret_cast<uint2*>(p + c) = w;
+    if constexpr (V == 2) {
+      auto bytes = [&](uint64_t v, int at, int n) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (e < n && at + e >= 0 && at + e < d) p[at + e] = static_cast<int8_t>(v >> 8 * e);
+      };
+      const uint64_t own = static_cast<uint64_t>(w.y) << 32 | w.x;
+      if (like) {
+        if (inside8(c, d)) *reinterpret_cast<uint2*>(p + c) = w;
+        else bytes(own, c, 8);
+      } else if (WARP) {
+        const int lane = threadIdx.x & 31, at = c + phase;  // at: a multiple of eight
+        const uint64_t next = __shfl_down_sync(0xffffffffu, own, 1);
+        const uint64_t v = phase ? own >> 8 * phase | next << (64 - 8 * phase) : own;
+        if (lane < 31 && at + 8 <= d) *reinterpret_cast<uint64_t*>(p + at) = v;
+        else bytes(v, at, lane < 31 ? 8 : 8 - phase);
+        if (lane == 0) bytes(own, c, phase);
+      } else {
+        bytes(own, c, 8);
+      }
+    } else if (FULL || c < d) {
+      *reinterpret_cast<uint2*>(p + c) = w;
+    }
   }
 }
 
@@ -306,14 +381,18 @@ struct RowsParams {
 template <typename T, bool NORM, int V, int K, bool FULL>
 __global__ void __launch_bounds__(NORM && K == 2 && V == 8 ? 512 : kRowThreads, NORM && (K == 4 || V == 1) ? 1 : 2)
     rows_kernel(const RowsParams p) {
+  extern __shared__ __align__(16) float gain_sm[];  // V = 2
   __shared__ BlockSums red[2];
   const T* xs = static_cast<const T*>(p.x);
   const T* rs = static_cast<const T*>(p.residual);
   T* hs = static_cast<T*>(p.h);
   T* ys = static_cast<T*>(p.y);
   constexpr int KR = K > 0 ? K : 1;
-  const int nt = blockDim.x, first = threadIdx.x * V, step = nt * 8, d = p.d;
-  const bool gain = NORM || p.gain;
+  const int nt = blockDim.x, step = nt * 8, d = p.d;
+  const int phase = V == 2 ? static_cast<int>(static_cast<int64_t>(blockIdx.x) * d & 7) : 0;
+  const int first = V == 2 ? threadIdx.x * 8 - phase : threadIdx.x * V;
+  const bool gain = NORM || p.gain, like = p.ldc == d;
+  if (V == 2 && gain) stage_gain(gain_sm, p.gain, phase, K > 0 ? K * step : (d + 14) / 8 * 8, d);
   clear_sums(red);
   Raw8<T, V> nx[KR], nr[NORM ? KR : 1];
   auto fetch = [&](int64_t row) {
@@ -352,7 +431,7 @@ __global__ void __launch_bounds__(NORM && K == 2 && V == 8 ? 512 : kRowThreads, 
     auto gained = [&](int c, float* v) {
       if (gain) {
         float g[8];
-        load8<float, V, FULL>(p.gain, c, nt, d, g);
+        load_gain<V, FULL>(p.gain, gain_sm, phase, c, nt, d, g);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] *= g[e];
       }
@@ -386,7 +465,7 @@ __global__ void __launch_bounds__(NORM && K == 2 && V == 8 ? 512 : kRowThreads, 
       if (NORM && p.rstd) p.rstd[row] = rstd;
     }
     auto finish = [&](int c, float* v) {
-      if (p.codes) store_codes<V, FULL>(p.codes + row * p.ldc, c, nt, d, v, sc);
+      if (p.codes) store_codes<V, FULL, (K > 0)>(p.codes + row * p.ldc, c, nt, d, v, sc, like, phase);
       if (NORM && ys) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] *= rstd;
@@ -428,21 +507,27 @@ struct NormGradParams {
 // HBM: 16384 x 4096 bf16 with dres 80 us, 82 at the copy rate.
 template <typename T, int V, int K, bool FULL>
 __global__ void __launch_bounds__(kRowThreads) norm_grad_kernel(const NormGradParams p) {
-  extern __shared__ float acc_sm[];  // K = 0
+  extern __shared__ __align__(16) float sm[];  // V = 2: gamma; K = 0: the share of dgamma behind it
   __shared__ BlockSums red[2];
   const T* dys = static_cast<const T*>(p.dy);
   const T* hs = static_cast<const T*>(p.h);
   const T* rs = static_cast<const T*>(p.dres);
   T* dxs = static_cast<T*>(p.dx);
   constexpr int KR = K > 0 ? K : 1;
-  const int nt = blockDim.x, first = threadIdx.x * V, step = nt * 8, d = p.d;
+  const int nt = blockDim.x, step = nt * 8, d = p.d;
+  const int phase = V == 2 ? static_cast<int>(static_cast<int64_t>(blockIdx.x) * d & 7) : 0;
+  const int first = V == 2 ? threadIdx.x * 8 - phase : threadIdx.x * V;
+  const int units = K > 0 ? K * step : (d + 14) / 8 * 8;
+  float* const acc_sm = V == 2 ? sm + units + phase : sm;
+  constexpr int VA = V == 2 ? 8 : V;  // the share of dgamma: whole units
   float acc[KR][8];
 #pragma unroll
   for (int k = 0; k < KR; ++k)
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[k][e] = 0.f;
   if constexpr (K == 0)
-    for (int c = first; c < d; c += step) store8<float, V, FULL>(acc_sm, c, nt, d, acc[0]);
+    for (int c = first; c < d; c += step) store8<float, VA, FULL>(acc_sm, c, nt, d, acc[0]);
+  if (V == 2) stage_gain(sm, p.gamma, phase, units, d);
   clear_sums(red);
   Raw8<T, V> ny[KR], nh[KR], nr[KR];
   float next_rstd = 0.f;
@@ -464,7 +549,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_grad_kernel(const NormGradPa
     const float rstd2[2] = {rstd, rstd};
     auto dots = [&](int c, float* a, float* b, float* w) {
       float g[8];
-      load8<float, V, FULL>(p.gamma, c, nt, d, g);
+      load_gain<V, FULL>(p.gamma, sm, phase, c, nt, d, g);
 #pragma unroll
       for (int e = 0; e < 8; e += 2) {
         mul2(b + e, rstd2);
@@ -487,9 +572,9 @@ __global__ void __launch_bounds__(kRowThreads) norm_grad_kernel(const NormGradPa
       for (int c = first; c < d; c += step) {
         load8<T, V, FULL>(dys + base, c, nt, d, dy[0]);
         load8<T, V, FULL>(hs + base, c, nt, d, h[0]);
-        load8<float, V, FULL>(acc_sm, c, nt, d, acc[0]);
+        load8<float, VA, FULL>(acc_sm, c, nt, d, acc[0]);
         dots(c, dy[0], h[0], acc[0]);
-        store8<float, V, FULL>(acc_sm, c, nt, d, acc[0]);
+        store8<float, VA, FULL>(acc_sm, c, nt, d, acc[0]);
       }
     }
     dot = dot2[0] + dot2[1];
@@ -517,7 +602,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_grad_kernel(const NormGradPa
         float g[8];
         load8<T, V, FULL>(dys + base, c, nt, d, dy[0]);
         load8<T, V, FULL>(hs + base, c, nt, d, h[0]);
-        load8<float, V, FULL>(p.gamma, c, nt, d, g);
+        load_gain<V, FULL>(p.gamma, sm, phase, c, nt, d, g);
         if (rs) fetch8<T, V, FULL>(nr[0], rs + base, c, nt, d);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -528,13 +613,13 @@ __global__ void __launch_bounds__(kRowThreads) norm_grad_kernel(const NormGradPa
       }
     }
   }
-  float* out = p.part + static_cast<int64_t>(blockIdx.x) * d;
+  float* out = p.part + static_cast<int64_t>(blockIdx.x) * d;  // (V = 2: a row like the others, blockIdx.x its number)
   if constexpr (K > 0) {
 #pragma unroll
     for (int k = 0; k < K; ++k) store8<float, V, FULL>(out, first + k * step, nt, d, acc[k]);
   } else {
     for (int c = first; c < d; c += step) {
-      load8<float, V, FULL>(acc_sm, c, nt, d, acc[0]);
+      load8<float, VA, FULL>(acc_sm, c, nt, d, acc[0]);
       store8<float, V, FULL>(out, c, nt, d, acc[0]);
     }
   }

@@ -197,6 +197,30 @@ def test_rmsnorm_backward(T, d, residual, dtype):
     assert out is acc and torch.equal(dx2, dx) and torch.equal(acc, 1 + dg)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,d", [(2500, 641), (1300, 1025), (900, 2261), (700, 4100), (400, 7169), (330, 14335), (310, 20001),
+                                 (5, 24577)])
+def test_rows_off_the_16_byte_units(T, d, dtype):
+    # rows of any start within a unit, several to a block, with and without a gain; rows
+    # of codes like the values' and on boundaries of their own (the gradient's)
+    x, r, gamma = rnd(50, T, d, dtype=dtype), rnd(51, T, d, dtype=dtype), rnd(52, d) + 1
+    q, s = px.quantize_rows(x)
+    qo, so = quantise64(x.float())
+    assert torch.equal(s, so) and torch.equal(q.double(), qo)
+    n = px.rmsnorm_quantize(x, gamma, r, EPS, y=True)
+    h = (x.float() + r.float()).to(dtype)
+    assert torch.equal(n.h, h) and torch.equal(n.codes.double(), quantise64(h.float() * gamma)[0])
+    y = (h.float() * gamma).double() * (h.double().square().mean(1, keepdim=True) + EPS).rsqrt()
+    k = chain(d)
+    within(n.y, y, (HALF[dtype] * (1 + k * U24) + (k + 1) * U24) * y.abs(), "y")
+    W = rnd(53, d, 48, scale=40).round().clamp(-127, 127).to(torch.int8)
+    qo, so = quantise64(x.float() * gamma)
+    want = (qo @ W.double()) * so.double()[:, None]
+    # the integer sum as fp32, times the scale, to the result's type
+    within(px.matmul_int8_grad(x, W, gamma), want, (HALF[dtype] + 2.01 * U24) * want.abs(), "dx")
+    test_rmsnorm_backward(T, d, True, dtype)
+
+
 def test_rmsnorm_gradient_by_differences():
     # the same loss in 64 bits, moved by +-e along one direction of x and of gamma
     T, d = 6, 48
