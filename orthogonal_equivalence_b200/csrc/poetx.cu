@@ -2587,7 +2587,7 @@ poetx_status poetx_rmsnorm_backward(int64_t T, int32_t d, const void* dy, const 
            POETX_CUDA(dtype == POETX_BF16 ? launch_norm_grad<__nv_bfloat16>(p, grid, r, st, dev)
                                           : launch_norm_grad<float>(p, grid, r, st, dev)));
   PROFILED(ST_NORM, st,
-           q8::sum_partials_kernel<<<(d + 31) / 32, 256, 0, st>>>(p.part, grid, d, dgamma, accumulate));
+           q8::sum_partials_kernel<<<(d + 31) / 32, 32 * q8::SLICES, 0, st>>>(p.part, grid, d, dgamma, accumulate));
   POETX_CUDA(cudaGetLastError());
   return POETX_OK;
 }
