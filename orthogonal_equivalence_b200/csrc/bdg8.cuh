@@ -40,8 +40,8 @@
 // released, and the next one loaded, before the last tile's dG; an item's first
 // O is computed while the dG before it is written.
 //
-// 16384 x 4096 takes 85 us with the sum of the splits (8 of them), 54 us without
-// O (53 and 32 us at the copy rate).  Neither HBM (48%) nor the tensor pipe (45%)
+// 16384 x 4096 takes 85 us with the sum of the nine splits, 54 us without
+// O (53 and 32 us at the copy rate).  Neither HBM (50%) nor the tensor pipe (48%)
 // is the bound, nor the conversion (left out: 80 and 52 us; with four warps 9 us
 // more): the O tiles' way through registers and boxes and the ends of the items
 // are; deeper rings of any of the three operands change nothing.
