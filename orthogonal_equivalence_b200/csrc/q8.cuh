@@ -659,6 +659,7 @@ __global__ void add_splits_kernel(const float* __restrict__ part, int splits, in
     float4* o4 = reinterpret_cast<float4*>(out);
     for (int64_t i = first; i < n / 4; i += step) {
       float4 a = p4[i];
+#pragma unroll 8
       for (int s = 1; s < splits; ++s) {
         const float4 v = p4[s * (n / 4) + i];
         a.x += v.x;
