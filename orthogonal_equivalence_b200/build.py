@@ -47,7 +47,7 @@ def build_tensors(force: bool = False) -> str:
     import sysconfig
 
     import torch
-    at = os.path.join(os.path.dirname(torch.__file__))
+    at = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
     tmp = f"{TENSORS}.{os.getpid()}.tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",

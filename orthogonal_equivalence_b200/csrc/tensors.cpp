@@ -2,7 +2,7 @@
 // call (include/poetx.h) of each function of quantized.py, in one step.  At the
 // smallest sizes a call is its host side (one token through the norm is 3 us on
 // the device), and the same steps in Python and ctypes take 9 to 15 us of it,
-// here 3 to 5.  No arithmetic: the C functions' addresses come from the library
+// here 4 to 7.  No arithmetic: the C functions' addresses come from the library
 // that the package has loaded.
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
