@@ -147,16 +147,17 @@ class PoetxLinear:
     def load(self, W0lin: torch.Tensor, permR: torch.Tensor, permP: torch.Tensor, qR: torch.Tensor,
              qP: torch.Tensor, stream=None) -> None:
         """Set the permutations and triangles, import the natural nn.Linear
-        weight W0^T ([n][m]) into the frame, and build G."""
+        weight W0^T ([n][m]) into the frame, and build G.  A layer that kept
+        its weight as codes is one with its weight in full again."""
         W0lin = W0lin.contiguous()
         _need(W0lin, (self.n, self.m), self.torch_dtype, self.device, "W0lin")
         for name, t, shape in (("permR", permR, self.permR.shape), ("permP", permP, self.permP.shape),
                                ("qR", qR, self.qR.shape), ("qP", qP, self.qP.shape)):
             if tuple(t.shape) != tuple(shape):
                 raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-        if self.int8_product:  # back to a layer that has its weight
+        if self.Wq is not None:  # W is the codes, or a scratch that the old codes would be expanded into
             self.W = torch.empty((self.n, self.m), dtype=self.torch_dtype, device=self.device)
-            self.Wq = self.Wscale = None
+            self.Wq = self.Wscale = self._wscratch = None
             self.int8_product = False
         self.permR.copy_(permR)
         self.permP.copy_(permP)

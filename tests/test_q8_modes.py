@@ -1,0 +1,77 @@
+"""A layer that changes between its forms: its weight in full, as int8 codes
+expanded before use (a scratch that several layers share), and as int8 codes
+that the W0 product multiplies.  Each change and each call of the weight has
+to see the layer's own weight, whatever the scratch holds."""
+import pytest
+import torch
+
+import orthogonal_equivalence_b200 as px
+from orthogonal_equivalence_b200 import build as pbuild
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def library():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    pbuild.build()
+    px.lib()
+    px.poetx_device_error()
+    yield
+    torch.cuda.synchronize()
+    assert px.poetx_device_error() == 0
+
+
+def rnd(seed, *shape, dtype=F32, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * scale).to(dtype).cuda()
+
+
+def state(m, n, b, dtype, seed):
+    """(W0, permR, permP, qR, qP) as PoetxLinear.load takes them."""
+    g = torch.Generator().manual_seed(100 + seed)
+    tri = b * (b - 1) // 2
+    return (rnd(101 + seed, n, m, dtype=dtype, scale=0.05), torch.randperm(m, generator=g).int().cuda(),
+            torch.randperm(n, generator=g).int().cuda(), rnd(102 + seed, m // b, tri, scale=0.02),
+            rnd(103 + seed, n // b, tri, scale=0.02))
+
+
+def layer(m, n, b, dtype, st):
+    L = px.PoetxLinear(m, n, b, px.POETX_BF16 if dtype == BF else px.POETX_FP32)
+    L.load(*st)
+    return L
+
+
+def two_on_one_scratch(m, n, b, dtype):
+    """A POET-XQ layer whose scratch another layer has used since, the states of both, and the other layer."""
+    st, other = state(m, n, b, dtype, 0), state(m, n, b, dtype, 50)
+    A, B = layer(m, n, b, dtype, st), layer(m, n, b, dtype, other)
+    scratch = torch.full((n * m,), float("nan"), dtype=dtype, device="cuda")
+    A.quantize_weight(scratch)
+    B.quantize_weight(scratch)
+    B.forward(rnd(9, 3, m, dtype=dtype))
+    return A, st, B, other
+
+
+FORMS = [(BF, 512, 768, 256, 70), (F32, 60, 90, 30, 50)]
+
+
+@pytest.mark.parametrize("dtype,m,n,b,T", FORMS)
+def test_a_new_weight_of_a_quantized_layer(dtype, m, n, b, T):
+    A, _, _, _ = two_on_one_scratch(m, n, b, dtype)
+    new = state(m, n, b, dtype, 80)
+    x, dz = rnd(1, T, m, dtype=dtype), rnd(2, T, n, dtype=dtype)
+    full = layer(m, n, b, dtype, new)
+    A.load(*new)
+    assert A.Wq is None and torch.equal(A.export_weight(), new[0])
+    for _ in range(2):      # in full, and quantized again
+        z, saved = full.forward(x)
+        z8, saved8 = A.forward(x)
+        assert torch.equal(z8, z)
+        for got, want in zip(A.backward(x, saved8, dz), full.backward(x, saved, dz)):
+            assert torch.equal(got, want)
+        if A.Wq is None:
+            A.quantize_weight()
+            full.quantize_weight()
