@@ -102,18 +102,21 @@ class PoetxLinear:
         scratch: the W0 product of the forward and of the backward multiplies
         the codes themselves with its other operand quantized row by row (see
         poetx_q8 in include/poetx.h); merge and export need the weight and
-        refuse then."""
+        refuse then.  A layer that already has codes keeps them: the call only
+        changes how they are used."""
         self._need_weight("quantize_weight")
         if int8_product and self.fold:
             raise ValueError("int8_product: the layer folds its blocks into the weight (fold != 0)")
         if int8_product and scratch is not None:
             raise ValueError("scratch: not used with int8_product")
-        self.Wq = torch.empty((self.n, self.m), dtype=torch.int8, device=self.device)
-        self.Wscale = torch.empty(self.n, dtype=torch.float32, device=self.device)
-        poetx_weight_quantize(self.n, self.m, self.W, self.dtype, self.Wq, self.Wscale, stream)
+        if self.Wq is None:  # (else W is the scratch, which holds any layer's weight or none)
+            self.Wq = torch.empty((self.n, self.m), dtype=torch.int8, device=self.device)
+            self.Wscale = torch.empty(self.n, dtype=torch.float32, device=self.device)
+            poetx_weight_quantize(self.n, self.m, self.W, self.dtype, self.Wq, self.Wscale, stream)
         self.int8_product = int8_product
         if int8_product:
             self.W = self.Wq  # (stands for the pointer only: no call of this mode reads it)
+            self._wscratch = None
             return
         if scratch is None:
             scratch = torch.empty(self.n * self.m, dtype=self.torch_dtype, device=self.device)

@@ -75,3 +75,35 @@ def test_a_new_weight_of_a_quantized_layer(dtype, m, n, b, T):
         if A.Wq is None:
             A.quantize_weight()
             full.quantize_weight()
+
+
+def expanded(W0):
+    """A natural weight after its rows went through int8 codes (a row keeps its
+    scale under any order of its columns)."""
+    n, m = W0.shape
+    q, s = torch.empty(n, m, dtype=torch.int8, device="cuda"), torch.empty(n, device="cuda")
+    px.poetx_weight_quantize(n, m, W0, px.POETX_BF16 if W0.dtype == BF else px.POETX_FP32, q, s)
+    return px.dequantize_rows(q, s, W0.dtype)
+
+
+@pytest.mark.parametrize("dtype,m,n,b,T", FORMS)
+def test_a_quantized_layer_takes_the_int8_product(dtype, m, n, b, T):
+    A, st, _, _ = two_on_one_scratch(m, n, b, dtype)
+    direct = layer(m, n, b, dtype, st)
+    direct.quantize_weight(int8_product=True)
+    A.quantize_weight(int8_product=True)
+    assert torch.equal(A.Wq, direct.Wq) and torch.equal(A.Wscale, direct.Wscale)
+    x, dz = rnd(1, T, m, dtype=dtype), rnd(2, T, n, dtype=dtype)
+    for got, want in zip(A.backward(x, A.forward(x)[1], dz), direct.backward(x, direct.forward(x)[1], dz)):
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype,m,n,b,T", FORMS)
+def test_a_quantized_layer_takes_another_scratch(dtype, m, n, b, T):
+    A, st, _, _ = two_on_one_scratch(m, n, b, dtype)
+    codes, scale = A.Wq.clone(), A.Wscale.clone()
+    A.quantize_weight()
+    assert torch.equal(A.Wq, codes) and torch.equal(A.Wscale, scale)
+    x = rnd(1, T, m, dtype=dtype)
+    want = layer(m, n, b, dtype, (expanded(st[0]), *st[1:])).forward(x)[0]
+    assert torch.equal(A.forward(x)[0], want)
