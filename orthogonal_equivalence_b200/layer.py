@@ -109,22 +109,21 @@ class PoetxLinear:
             raise ValueError("int8_product: the layer folds its blocks into the weight (fold != 0)")
         if int8_product and scratch is not None:
             raise ValueError("scratch: not used with int8_product")
+        if not int8_product:
+            if scratch is None:
+                scratch = torch.empty(self.n * self.m, dtype=self.torch_dtype, device=self.device)
+            if scratch.numel() < self.n * self.m:
+                raise ValueError(f"scratch: {scratch.numel()} elements, the layer needs {self.n * self.m}")
+            _need(scratch, (scratch.numel(),), self.torch_dtype, self.device, "scratch")
         if self.Wq is None:  # (else W is the scratch, which holds any layer's weight or none)
-            self.Wq = torch.empty((self.n, self.m), dtype=torch.int8, device=self.device)
-            self.Wscale = torch.empty(self.n, dtype=torch.float32, device=self.device)
-            poetx_weight_quantize(self.n, self.m, self.W, self.dtype, self.Wq, self.Wscale, stream)
+            Wq = torch.empty((self.n, self.m), dtype=torch.int8, device=self.device)
+            Wscale = torch.empty(self.n, dtype=torch.float32, device=self.device)
+            poetx_weight_quantize(self.n, self.m, self.W, self.dtype, Wq, Wscale, stream)
+            self.Wq, self.Wscale = Wq, Wscale
         self.int8_product = int8_product
-        if int8_product:
-            self.W = self.Wq  # (stands for the pointer only: no call of this mode reads it)
-            self._wscratch = None
-            return
-        if scratch is None:
-            scratch = torch.empty(self.n * self.m, dtype=self.torch_dtype, device=self.device)
-        if scratch.numel() < self.n * self.m:
-            raise ValueError(f"scratch: {scratch.numel()} elements, the layer needs {self.n * self.m}")
-        _need(scratch, (scratch.numel(),), self.torch_dtype, self.device, "scratch")
         self._wscratch = scratch
-        self.W = scratch[: self.n * self.m].view(self.n, self.m)
+        # (int8_product: W stands for the pointer only, no call of this mode reads it)
+        self.W = self.Wq if int8_product else scratch[: self.n * self.m].view(self.n, self.m)
 
     def _dequantize(self, stream=None) -> None:
         if self.Wq is not None and not self.int8_product:
