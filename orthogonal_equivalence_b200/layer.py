@@ -187,6 +187,7 @@ class PoetxLinear:
 
     def export_weight(self, stream=None) -> torch.Tensor:
         self._need_weight("export_weight")
+        self._dequantize(stream)
         out = torch.empty((self.n, self.m), dtype=self.torch_dtype, device=self.device)
         poetx_frame_export(self.abi(), out, stream)
         return out

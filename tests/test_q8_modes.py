@@ -107,3 +107,10 @@ def test_a_quantized_layer_takes_another_scratch(dtype, m, n, b, T):
     x = rnd(1, T, m, dtype=dtype)
     want = layer(m, n, b, dtype, (expanded(st[0]), *st[1:])).forward(x)[0]
     assert torch.equal(A.forward(x)[0], want)
+
+
+@pytest.mark.parametrize("dtype,m,n,b,T", FORMS)
+def test_the_weight_of_a_quantized_layer_is_exported(dtype, m, n, b, T):
+    A, st, B, other = two_on_one_scratch(m, n, b, dtype)
+    for L, s in ((A, st), (B, other), (A, st)):
+        assert torch.equal(L.export_weight(), expanded(s[0]))
