@@ -330,8 +330,10 @@ class PoetxLinear:
 
     def merge(self, new_permR: torch.Tensor, new_permP: torch.Tensor, stream=None) -> None:
         """W0 <- R W0 P, re-expressed in the frame of the new permutations;
-        q = 0 and G = I afterwards."""
+        q = 0 and G = I afterwards.  The merged weight of a quantized layer is
+        quantized again, into the same codes and scales."""
         self._need_weight("merge")
+        self._dequantize(stream)
         L = self.abi()
         nb = poetx_merge_workspace_bytes(L)
         ws = self.workspace("merge", nb)
@@ -341,7 +343,10 @@ class PoetxLinear:
         _need(newR, (self.m,), torch.int32, self.device, "new_permR")
         _need(newP, (self.n,), torch.int32, self.device, "new_permP")
         poetx_merge(L, newR, newP, W_out, ws, nb, stream)
-        self.W = W_out
+        if self.Wq is None:
+            self.W = W_out
+        else:
+            poetx_weight_quantize(self.n, self.m, W_out, self.dtype, self.Wq, self.Wscale, stream)
         self.permR.copy_(newR)
         self.permP.copy_(newP)
 

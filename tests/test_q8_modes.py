@@ -114,3 +114,29 @@ def test_the_weight_of_a_quantized_layer_is_exported(dtype, m, n, b, T):
     A, st, B, other = two_on_one_scratch(m, n, b, dtype)
     for L, s in ((A, st), (B, other), (A, st)):
         assert torch.equal(L.export_weight(), expanded(s[0]))
+
+
+@pytest.mark.parametrize("dtype,m,n,b,T", FORMS)
+def test_a_quantized_layer_is_merged(dtype, m, n, b, T):
+    A, st, B, other = two_on_one_scratch(m, n, b, dtype)
+    new = state(m, n, b, dtype, 80)[1:3]
+    x, dz = rnd(1, T, m, dtype=dtype), rnd(2, T, n, dtype=dtype)
+    for L, s in ((A, st), (B, other)):
+        full = layer(m, n, b, dtype, (expanded(s[0]), *s[1:]))
+        full.merge(*new)
+        merged = full.W.clone()
+        full.quantize_weight()
+        L.merge(*new)
+        assert torch.equal(L.Wq, full.Wq) and torch.equal(L.Wscale, full.Wscale)
+        assert torch.equal(L.permR, new[0]) and torch.equal(L.permP, new[1]) and not L.qR.any() and not L.qP.any()
+        # what the codes stand for is the merged weight to half a step, and the bf16 rounding of that
+        assert ((L.export_weight()[new[1].long()][:, new[0].long()].double() - merged.double()).abs() <=
+                (0.5 + 127 * 2.0 ** -8) * L.Wscale.double()[:, None] * (1 + 1e-6)).all()
+    for L, s in ((A, st), (B, other)):
+        z, saved = L.forward(x)
+        W = px.dequantize_rows(L.Wq, L.Wscale, dtype)          # in the frame: G = I and z = Xg W^T there
+        want = x[:, new[0].long()].double() @ W.double().t()
+        size = x[:, new[0].long()].double().abs() @ W.double().abs().t()
+        # m fp32 sums (up to a whole step each on the tensor cores), one rounding to dtype
+        half = 2.0 ** -8 if dtype == BF else 2.0 ** -24
+        assert ((z[:, new[1].long()].double() - want).abs() <= half * want.abs() + 2 * (m + 2) * 2.0 ** -24 * size).all()
