@@ -55,6 +55,14 @@ def _workspace(held: dict, kind: str, nbytes: int, device: torch.device) -> torc
     return ws
 
 
+def _torch_stream(stream, device: torch.device):
+    """The torch stream of a call's `stream` argument (a stream or its handle); None where none is given."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = stream if isinstance(stream, int) else stream.cuda_stream
+    return torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+
+
 class Saved(NamedTuple):
     """Activations the forward keeps for the backward: Y ([T][n], the P-side
     input in the Psi_P frame) and optionally Xg ([T][m], x in the Psi_R frame),
@@ -374,19 +382,31 @@ class Int8Linear:
 
     @classmethod
     def from_layer(cls, layer: PoetxLinear, stream=None) -> "Int8Linear":
+        """The served form of a layer.  With `stream` the work runs there, after
+        what the current stream holds and before what is queued on it later."""
         layer._need_weight("from_layer")
-        layer._dequantize(stream)
-        # merge a copy of the layer's state into the natural order (identity permutations)
-        keep = [t.clone() for t in (layer.qR, layer.qP, layer.GR, layer.GP)]
-        L = make_layer(layer.m, layer.n, layer.b, layer.dtype, layer.W, layer.permR, layer.permP, *keep)
-        eyeR = torch.arange(layer.m, dtype=torch.int32, device=layer.device)
-        eyeP = torch.arange(layer.n, dtype=torch.int32, device=layer.device)
-        W = torch.empty((layer.n, layer.m), dtype=layer.torch_dtype, device=layer.device)
-        nb = poetx_merge_workspace_bytes(L)
-        ws = torch.empty(max(nb, 1), dtype=torch.uint8, device=layer.device)
-        with torch.cuda.device(W.device):
-            poetx_merge(L, eyeR, eyeP, W, ws, nb, stream)
-        return cls(W, stream)
+        here = torch.cuda.current_stream(layer.device)
+        there = _torch_stream(stream, layer.device) or here
+        if there != here:
+            there.wait_stream(here)
+        # every copy and temporary belongs to the stream that uses it
+        with torch.cuda.device(layer.device), torch.cuda.stream(there):
+            layer._dequantize(there)
+            # merge a copy of the layer's state into the natural order (identity permutations)
+            keep = [t.clone() for t in (layer.qR, layer.qP, layer.GR, layer.GP)]
+            L = make_layer(layer.m, layer.n, layer.b, layer.dtype, layer.W, layer.permR, layer.permP, *keep)
+            eyeR = torch.arange(layer.m, dtype=torch.int32, device=layer.device)
+            eyeP = torch.arange(layer.n, dtype=torch.int32, device=layer.device)
+            W = torch.empty((layer.n, layer.m), dtype=layer.torch_dtype, device=layer.device)
+            nb = poetx_merge_workspace_bytes(L)
+            ws = torch.empty(max(nb, 1), dtype=torch.uint8, device=layer.device)
+            poetx_merge(L, eyeR, eyeP, W, ws, nb, there)
+            lin = cls(W, there)
+        if there != here:
+            here.wait_stream(there)
+            for t in (lin.Wq, lin.wscale):
+                t.record_stream(here)
+        return lin
 
     def forward(self, x) -> torch.Tensor:
         """z [T][n] from tokens [T][m] (quantized here) or from their int8 rows

@@ -140,3 +140,45 @@ def test_a_quantized_layer_is_merged(dtype, m, n, b, T):
         # m fp32 sums (up to a whole step each on the tensor cores), one rounding to dtype
         half = 2.0 ** -8 if dtype == BF else 2.0 ** -24
         assert ((z[:, new[1].long()].double() - want).abs() <= half * want.abs() + 2 * (m + 2) * 2.0 ** -24 * size).all()
+
+
+@pytest.mark.parametrize("quantized", [False, True])
+@pytest.mark.parametrize("handle", [False, True])
+def test_a_served_linear_made_on_another_stream(handle, quantized):
+    # either stream is kept busy in turn, so that work that is not ordered between the two would be seen: the
+    # layer's last change is still to come on the current stream, and memory that the call gives back is used there
+    m, n, b = 512, 768, 256
+    st = state(m, n, b, BF, 0)
+    L = layer(m, n, b, BF, st)
+    if quantized:
+        L.quantize_weight()
+    want = px.Int8Linear.from_layer(L)
+    L.qR.zero_()
+    L.build()
+    side = torch.cuda.Stream()
+    for _ in range(2):                   # (the second one finds the allocator's memory used)
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)
+        L.qR.copy_(st[3])
+        L.build()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(40_000_000)
+        lin = px.Int8Linear.from_layer(L, stream=side.cuda_stream if handle else side)
+        junk = [torch.full((s,), 77, dtype=torch.uint8, device="cuda") for s in (m * n * 2, m * n * 8, m * 4, n * 4) * 4]
+        got = lin.Wq.clone(), lin.wscale.clone()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want.Wq) and torch.equal(got[1], want.wscale)
+        assert all(bool((j == 77).all()) for j in junk)
+        L.qR.zero_()
+        L.build()
+
+
+def test_a_served_linear_made_on_the_default_stream_from_another():
+    L = layer(512, 768, 256, BF, state(512, 768, 256, BF, 0))
+    want = px.Int8Linear.from_layer(L)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        lin = px.Int8Linear.from_layer(L, stream=0)
+        same = torch.equal(lin.Wq, want.Wq) and torch.equal(lin.wscale, want.wscale)
+    assert same
