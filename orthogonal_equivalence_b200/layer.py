@@ -8,6 +8,7 @@ triangles qR, qP (the trainable parameters) and the G blocks built from them.
 """
 from __future__ import annotations
 
+import contextlib
 from typing import NamedTuple, Optional, Tuple, Union
 
 import torch
@@ -41,26 +42,29 @@ def _need(t, shape, dtype, device: torch.device, name: str) -> None:
         raise ValueError(f"{name}: must be contiguous")
 
 
-def _workspace(held: dict, kind: str, nbytes: int, device: torch.device) -> torch.Tensor:
-    """Scratch of a call: held and reused by eager calls (which are therefore
-    to be ordered on one stream), but a captured call's own, from its graph's
-    memory, so that no two graphs share it and no later eager call that needs
-    more can free it under a graph."""
-    if device.type == "cuda" and torch.cuda.is_current_stream_capturing():
-        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
-    ws = held.get(kind)
-    if ws is None or ws.numel() < nbytes:
-        ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
-        held[kind] = ws
-    return ws
-
-
 def _torch_stream(stream, device: torch.device):
     """The torch stream of a call's `stream` argument (a stream or its handle); None where none is given."""
     if stream is None or isinstance(stream, torch.cuda.Stream):
         return stream
     handle = stream if isinstance(stream, int) else stream.cuda_stream
     return torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+
+
+def _workspace(held: dict, kind: str, nbytes: int, device: torch.device, stream=None) -> torch.Tensor:
+    """Scratch of a call on `stream`: held and reused by eager calls (which are
+    therefore to be ordered on one stream), but a captured call's own, from its
+    graph's memory, so that no two graphs share it and no later eager call that
+    needs more can free it under a graph.  It is allocated on the call's
+    stream, which is therefore the only one that can get its memory next."""
+    on_gpu = device.type == "cuda"
+    with torch.cuda.stream(_torch_stream(stream, device)) if on_gpu else contextlib.nullcontext():
+        if on_gpu and torch.cuda.is_current_stream_capturing():
+            return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+        ws = held.get(kind)
+        if ws is None or ws.numel() < nbytes:
+            ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+            held[kind] = ws
+        return ws
 
 
 class Saved(NamedTuple):
@@ -150,8 +154,8 @@ class PoetxLinear:
         return make_layer(self.m, self.n, self.b, self.dtype, self.W, self.permR, self.permP, self.qR, self.qP,
                           self.GR, self.GP, self.fold)
 
-    def workspace(self, kind: str, nbytes: int) -> torch.Tensor:
-        return _workspace(self._ws, kind, nbytes, self.device)
+    def workspace(self, kind: str, nbytes: int, stream=None) -> torch.Tensor:
+        return _workspace(self._ws, kind, nbytes, self.device, stream)
 
     # -------------------------------------------------------------- state
     def load(self, W0lin: torch.Tensor, permR: torch.Tensor, permP: torch.Tensor, qR: torch.Tensor,
@@ -204,7 +208,7 @@ class PoetxLinear:
         """G_R, G_P from qR, qP (Cayley-Neumann), both sides in one batch."""
         L = self._abi()
         nb = poetx_layer_cnp_workspace_bytes(L)
-        ws = self.workspace("cnp", nb)
+        ws = self.workspace("cnp", nb, stream)
         poetx_layer_cnp_build(L, ws, nb, stream)
 
     # -------------------------------------------------------------- layer
@@ -241,11 +245,11 @@ class PoetxLinear:
         q8 = self._q8(y, xg)
         if q8 is None:
             nb = poetx_forward_workspace_bytes(L, T)
-            ws = self.workspace("fwd", nb)
+            ws = self.workspace("fwd", nb, stream)
             poetx_forward(L, T, x, z, y, xg, ws, nb, stream)
         else:
             nb = poetx_forward_q8_workspace_bytes(L, T, q8)
-            ws = self.workspace("fwd", nb)
+            ws = self.workspace("fwd", nb, stream)
             with torch.cuda.device(x.device):
                 poetx_forward_q8(L, T, x, z, None if save8 else y, None if save8 else xg, q8, ws, nb, stream)
         return z, (Saved(y, xg) if save else None)
@@ -313,11 +317,11 @@ class PoetxLinear:
         xg = None if isinstance(saved.xg, Checkpoint) else saved.xg
         if q8 is None:
             nb = (poetx_backward_workspace_bytes if y is not None else poetx_backward_recompute_workspace_bytes)(L, T)
-            ws = self.workspace("bwd", nb)
+            ws = self.workspace("bwd", nb, stream)
             call(L, T, x, y, xg, dz, dx, gR, gP, int(accumulate), ws, nb, stream)
         else:
             nb = poetx_backward_q8_workspace_bytes(L, T, int(y is not None), q8)
-            ws = self.workspace("bwd", nb)
+            ws = self.workspace("bwd", nb, stream)
             with torch.cuda.device(dz.device):
                 call_q8(L, T, x, y, xg, q8, dz, dx, gR, gP, int(accumulate), ws, nb, stream)
 
@@ -344,7 +348,7 @@ class PoetxLinear:
         self._dequantize(stream)
         L = self.abi()
         nb = poetx_merge_workspace_bytes(L)
-        ws = self.workspace("merge", nb)
+        ws = self.workspace("merge", nb, stream)
         W_out = torch.empty_like(self.W)
         newR = new_permR.to(device=self.device, dtype=torch.int32).contiguous()
         newP = new_permP.to(device=self.device, dtype=torch.int32).contiguous()
@@ -489,11 +493,11 @@ class LayerGroup:
         _need(dG, (nblk, L0.b, L0.b), torch.float32, self.q.device, "dG")
         _need(dq, tuple(self.q.shape), torch.float32, self.q.device, "dq")
         nb = poetx_cnp_workspace_bytes(nblk, L0.b, L0.dtype)
-        ws = _workspace(self._ws, "bwd", nb, L0.device)
+        ws = _workspace(self._ws, "bwd", nb, L0.device, stream)
         poetx_cnp_backward(nblk, L0.b, self.q, dG, dq, int(accumulate), L0.dtype, ws, nb, stream)
 
     def build(self, stream=None) -> None:
         abis = [L._abi() for L in self.layers]
         nb = poetx_layers_cnp_workspace_bytes(abis)
-        ws = _workspace(self._ws, "build", nb, self.layers[0].device)
+        ws = _workspace(self._ws, "build", nb, self.layers[0].device, stream)
         poetx_layers_cnp_build(abis, ws, nb, stream)

@@ -21,3 +21,67 @@ def test_a_refused_scratch_leaves_the_layer_as_it_was(monkeypatch, scratch, matc
     with pytest.raises(ValueError, match=match):
         L.quantize_weight(scratch)
     assert L.W is W and L.Wq is None and L.Wscale is None
+
+
+class Streams:
+    """torch's streams stood in for: allocations note the stream that is current."""
+
+    def __init__(self, monkeypatch, capturing):
+        self.current, self.made = "current", []
+        empty = torch.empty
+
+        class On:
+            def __init__(on, s):
+                on.s = s
+
+            def __enter__(on):
+                on.was = self.current
+                self.current = on.s or on.was
+
+            def __exit__(on, *a):
+                self.current = on.was
+
+        def made(*a, device=None, **k):
+            t = empty(*a, **k)
+            self.made.append((t, self.current))
+            return t
+
+        monkeypatch.setattr(torch.cuda, "stream", On)
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing)
+        monkeypatch.setattr(torch, "empty", made)
+        monkeypatch.setattr(layer_py, "_torch_stream", lambda s, device: s, raising=False)
+
+
+@pytest.mark.parametrize("capturing", [False, True])
+def test_scratch_belongs_to_the_stream_that_uses_it(monkeypatch, capturing):
+    # freed scratch (a captured call's at its end, an eager one's when a larger one takes its place) goes back to
+    # the stream it was made on: another one than the call's could hand it out while the call still runs
+    s = Streams(monkeypatch, capturing)
+    cuda, held = torch.device("cuda", 0), {}
+    layer_py._workspace(held, "fwd", 100, cuda, "side")
+    layer_py._workspace(held, "fwd", 200, cuda, "side")
+    layer_py._workspace(held, "bwd", 100, cuda, None)
+    assert [(t.numel(), on) for t, on in s.made] == [(100, "side"), (200, "side"), (100, "current")]
+    assert not capturing or not held
+
+
+def test_every_call_asks_for_scratch_on_its_stream(monkeypatch):
+    L = px.PoetxLinear(128, 192, 64, px.POETX_BF16, device="cpu")
+    group = px.LayerGroup([L])
+    group.flatten_params()
+    asked = []
+    workspace = layer_py._workspace
+    monkeypatch.setattr(layer_py, "_workspace", lambda *a: (asked.append(a[1:2] + a[4:]), workspace(*a[:4]))[1])
+    for name in ("poetx_forward", "poetx_backward", "poetx_backward_dG", "poetx_layer_cnp_build", "poetx_merge",
+                 "poetx_layers_cnp_build", "poetx_cnp_backward", "poetx_frame_import"):
+        monkeypatch.setattr(layer_py, name, lambda *a: None)
+    x, dz = torch.zeros(4, 128, dtype=BF), torch.zeros(4, 192, dtype=BF)
+    dG = group.dG_buffer()
+    L.forward(x, stream="side")
+    L.backward(x, None, dz, stream="side")
+    L.backward_dG(x, None, dz, *group.dG_views(dG)[0], stream="side")
+    L.build(stream="side")
+    L.merge(L.permR, L.permP, stream="side")
+    group.build(stream="side")
+    group.cnp_backward(dG, torch.zeros_like(group.q), stream="side")
+    assert asked == [(k, "side") for k in ("fwd", "bwd", "bwd", "cnp", "merge", "build", "bwd")]

@@ -182,3 +182,40 @@ def test_a_served_linear_made_on_the_default_stream_from_another():
         lin = px.Int8Linear.from_layer(L, stream=0)
         same = torch.equal(lin.Wq, want.Wq) and torch.equal(lin.wscale, want.wscale)
     assert same
+
+
+@pytest.mark.parametrize("int8_product", [False, True])
+def test_two_layers_on_two_streams_of_one_graph(int8_product):
+    # a graph that forks: one layer on a given stream, the other on the graph's own, with nothing between them
+    # but the join, and scratch of the same sizes
+    T, m, n = 700, 512, 768
+    layers = [layer(m, n, 256, BF, state(m, n, 256, BF, 30 * i)) for i in range(2)]
+    ins = [(rnd(1 + i, T, m, dtype=BF), rnd(11 + i, T, n, dtype=BF)) for i in range(2)]
+    if int8_product:
+        for L in layers:
+            L.quantize_weight(int8_product=True)
+
+    def step(i, stream=None):
+        x, dz = ins[i]
+        z, saved = layers[i].forward(x, save_xg=True, stream=stream)
+        return (z, *layers[i].backward(None, saved, dz, stream=stream)), saved
+
+    want = [step(i)[0] for i in range(2)]
+    torch.cuda.synchronize()
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        out = [None, None]
+        out[0], held = step(0, side)     # (what the caller holds, it holds until the join)
+        out[1], _ = step(1)
+        here.wait_stream(side)
+        del held
+    for _ in range(4):
+        for o in out:
+            for t in o:
+                t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for o, w in zip(out, want):
+            assert all(torch.equal(a, b) for a, b in zip(o, w))
