@@ -50,15 +50,25 @@ def _torch_stream(stream, device: torch.device):
     return torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
 
 
+def _on(stream, device: torch.device):
+    """A context in which torch's own work and allocations belong to the stream a call is given."""
+    return torch.cuda.stream(_torch_stream(stream, device)) if device.type == "cuda" else contextlib.nullcontext()
+
+
+def _drop(t: torch.Tensor, stream) -> None:
+    """`t` is let go while a call on `stream` may still read it."""
+    if stream is not None and t.device.type == "cuda":
+        t.record_stream(_torch_stream(stream, t.device))
+
+
 def _workspace(held: dict, kind: str, nbytes: int, device: torch.device, stream=None) -> torch.Tensor:
     """Scratch of a call on `stream`: held and reused by eager calls (which are
     therefore to be ordered on one stream), but a captured call's own, from its
     graph's memory, so that no two graphs share it and no later eager call that
     needs more can free it under a graph.  It is allocated on the call's
     stream, which is therefore the only one that can get its memory next."""
-    on_gpu = device.type == "cuda"
-    with torch.cuda.stream(_torch_stream(stream, device)) if on_gpu else contextlib.nullcontext():
-        if on_gpu and torch.cuda.is_current_stream_capturing():
+    with _on(stream, device):
+        if device.type == "cuda" and torch.cuda.is_current_stream_capturing():
             return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
         ws = held.get(kind)
         if ws is None or ws.numel() < nbytes:
@@ -131,6 +141,7 @@ class PoetxLinear:
             Wq = torch.empty((self.n, self.m), dtype=torch.int8, device=self.device)
             Wscale = torch.empty(self.n, dtype=torch.float32, device=self.device)
             poetx_weight_quantize(self.n, self.m, self.W, self.dtype, Wq, Wscale, stream)
+            _drop(self.W, stream)
             self.Wq, self.Wscale = Wq, Wscale
         self.int8_product = int8_product
         self._wscratch = scratch
@@ -163,7 +174,8 @@ class PoetxLinear:
         """Set the permutations and triangles, import the natural nn.Linear
         weight W0^T ([n][m]) into the frame, and build G.  A layer that kept
         its weight as codes is one with its weight in full again."""
-        W0lin = W0lin.contiguous()
+        with _on(stream, self.device):
+            W0lin = W0lin.contiguous()
         _need(W0lin, (self.n, self.m), self.torch_dtype, self.device, "W0lin")
         for name, t, shape in (("permR", permR, self.permR.shape), ("permP", permP, self.permP.shape),
                                ("qR", qR, self.qR.shape), ("qP", qP, self.qP.shape)):
@@ -173,10 +185,11 @@ class PoetxLinear:
             self.W = torch.empty((self.n, self.m), dtype=self.torch_dtype, device=self.device)
             self.Wq = self.Wscale = self._wscratch = None
             self.int8_product = False
-        self.permR.copy_(permR)
-        self.permP.copy_(permP)
-        self.qR.copy_(qR)
-        self.qP.copy_(qP)
+        with _on(stream, self.device):
+            self.permR.copy_(permR)
+            self.permP.copy_(permP)
+            self.qR.copy_(qR)
+            self.qP.copy_(qP)
         poetx_frame_import(self.abi(), W0lin, stream)
         self.build(stream)
 
@@ -349,18 +362,20 @@ class PoetxLinear:
         L = self.abi()
         nb = poetx_merge_workspace_bytes(L)
         ws = self.workspace("merge", nb, stream)
-        W_out = torch.empty_like(self.W)
-        newR = new_permR.to(device=self.device, dtype=torch.int32).contiguous()
-        newP = new_permP.to(device=self.device, dtype=torch.int32).contiguous()
-        _need(newR, (self.m,), torch.int32, self.device, "new_permR")
-        _need(newP, (self.n,), torch.int32, self.device, "new_permP")
-        poetx_merge(L, newR, newP, W_out, ws, nb, stream)
-        if self.Wq is None:
-            self.W = W_out
-        else:
-            poetx_weight_quantize(self.n, self.m, W_out, self.dtype, self.Wq, self.Wscale, stream)
-        self.permR.copy_(newR)
-        self.permP.copy_(newP)
+        with _on(stream, self.device):
+            W_out = torch.empty_like(self.W)
+            newR = new_permR.to(device=self.device, dtype=torch.int32).contiguous()
+            newP = new_permP.to(device=self.device, dtype=torch.int32).contiguous()
+            _need(newR, (self.m,), torch.int32, self.device, "new_permR")
+            _need(newP, (self.n,), torch.int32, self.device, "new_permP")
+            poetx_merge(L, newR, newP, W_out, ws, nb, stream)
+            if self.Wq is None:
+                _drop(self.W, stream)
+                self.W = W_out
+            else:
+                poetx_weight_quantize(self.n, self.m, W_out, self.dtype, self.Wq, self.Wscale, stream)
+            self.permR.copy_(newR)
+            self.permP.copy_(newP)
 
 
 class Int8Linear:

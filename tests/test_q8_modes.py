@@ -219,3 +219,29 @@ def test_two_layers_on_two_streams_of_one_graph(int8_product):
         torch.cuda.synchronize()
         for o, w in zip(out, want):
             assert all(torch.equal(a, b) for a, b in zip(o, w))
+
+
+def test_load_merge_and_quantize_on_another_stream():
+    # the current stream is busy: what these calls do with torch has to go to the stream they are given, too
+    m, n, b = 512, 768, 256
+    first, st, new = state(m, n, b, BF, 0), state(m, n, b, BF, 50), state(m, n, b, BF, 80)[1:3]
+    x = rnd(1, 40, m, dtype=BF)
+    full = layer(m, n, b, BF, st)
+    full.merge(*new)
+    want = full.forward(x)[0]
+    full.quantize_weight()
+    want8 = full.forward(x)[0]
+    L, side = layer(m, n, b, BF, first), torch.cuda.Stream()
+    new64 = [p.long() for p in new]       # (converted by the call)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(60_000_000)
+    L.load(*st, stream=side)
+    L.merge(*new64, stream=side)
+    z = L.forward(x, stream=side)[0]
+    L.quantize_weight(stream=side)
+    z8 = L.forward(x, stream=side)[0]
+    side.synchronize()
+    with torch.cuda.stream(side):
+        same = torch.equal(z, want), torch.equal(z8, want8), torch.equal(L.Wq, full.Wq)
+    assert same == (True, True, True)
+    torch.cuda.synchronize()
