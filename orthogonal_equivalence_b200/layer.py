@@ -51,8 +51,13 @@ def _torch_stream(stream, device: torch.device):
 
 
 def _on(stream, device: torch.device):
-    """A context in which torch's own work and allocations belong to the stream a call is given."""
-    return torch.cuda.stream(_torch_stream(stream, device)) if device.type == "cuda" else contextlib.nullcontext()
+    """A context in which `device` is the current one and torch's own work and
+    allocations belong to the stream a call is given (the device's current one
+    where it is given none): the C calls run on the current device."""
+    if device.type != "cuda":
+        return contextlib.nullcontext()
+    s = _torch_stream(stream, device)
+    return torch.cuda.device(device) if s is None else torch.cuda.stream(s)
 
 
 def _drop(t: torch.Tensor, stream) -> None:
@@ -140,7 +145,8 @@ class PoetxLinear:
         if self.Wq is None:  # (else W is the scratch, which holds any layer's weight or none)
             Wq = torch.empty((self.n, self.m), dtype=torch.int8, device=self.device)
             Wscale = torch.empty(self.n, dtype=torch.float32, device=self.device)
-            poetx_weight_quantize(self.n, self.m, self.W, self.dtype, Wq, Wscale, stream)
+            with self._on(stream):
+                poetx_weight_quantize(self.n, self.m, self.W, self.dtype, Wq, Wscale, stream)
             _drop(self.W, stream)
             self.Wq, self.Wscale = Wq, Wscale
         self.int8_product = int8_product
@@ -165,6 +171,9 @@ class PoetxLinear:
         return make_layer(self.m, self.n, self.b, self.dtype, self.W, self.permR, self.permP, self.qR, self.qP,
                           self.GR, self.GP, self.fold)
 
+    def _on(self, stream):
+        return _on(stream, self.permR.device)
+
     def workspace(self, kind: str, nbytes: int, stream=None) -> torch.Tensor:
         return _workspace(self._ws, kind, nbytes, self.device, stream)
 
@@ -174,7 +183,7 @@ class PoetxLinear:
         """Set the permutations and triangles, import the natural nn.Linear
         weight W0^T ([n][m]) into the frame, and build G.  A layer that kept
         its weight as codes is one with its weight in full again."""
-        with _on(stream, self.device):
+        with self._on(stream):
             W0lin = W0lin.contiguous()
         _need(W0lin, (self.n, self.m), self.torch_dtype, self.device, "W0lin")
         for name, t, shape in (("permR", permR, self.permR.shape), ("permP", permP, self.permP.shape),
@@ -185,12 +194,12 @@ class PoetxLinear:
             self.W = torch.empty((self.n, self.m), dtype=self.torch_dtype, device=self.device)
             self.Wq = self.Wscale = self._wscratch = None
             self.int8_product = False
-        with _on(stream, self.device):
+        with self._on(stream):
             self.permR.copy_(permR)
             self.permP.copy_(permP)
             self.qR.copy_(qR)
             self.qP.copy_(qP)
-        poetx_frame_import(self.abi(), W0lin, stream)
+            poetx_frame_import(self.abi(), W0lin, stream)
         self.build(stream)
 
     def _need_weight(self, what: str) -> None:
@@ -212,17 +221,19 @@ class PoetxLinear:
 
     def export_weight(self, stream=None) -> torch.Tensor:
         self._need_weight("export_weight")
-        self._dequantize(stream)
         out = torch.empty((self.n, self.m), dtype=self.torch_dtype, device=self.device)
-        poetx_frame_export(self.abi(), out, stream)
+        with self._on(stream):
+            self._dequantize(stream)
+            poetx_frame_export(self.abi(), out, stream)
         return out
 
     def build(self, stream=None) -> None:
         """G_R, G_P from qR, qP (Cayley-Neumann), both sides in one batch."""
-        L = self._abi()
-        nb = poetx_layer_cnp_workspace_bytes(L)
-        ws = self.workspace("cnp", nb, stream)
-        poetx_layer_cnp_build(L, ws, nb, stream)
+        with self._on(stream):
+            L = self._abi()
+            nb = poetx_layer_cnp_workspace_bytes(L)
+            ws = self.workspace("cnp", nb, stream)
+            poetx_layer_cnp_build(L, ws, nb, stream)
 
     # -------------------------------------------------------------- layer
     def forward(self, x: torch.Tensor, save: bool = True, save_xg: bool = False, z: Optional[torch.Tensor] = None,
@@ -253,17 +264,17 @@ class PoetxLinear:
         for name, t, d in (("y", y, self.n), ("xg", xg, self.m)):
             if t is not None:
                 self._need_saved(t, T, d, name, save8)
-        self._dequantize(stream)
-        L = self._abi()
-        q8 = self._q8(y, xg)
-        if q8 is None:
-            nb = poetx_forward_workspace_bytes(L, T)
-            ws = self.workspace("fwd", nb, stream)
-            poetx_forward(L, T, x, z, y, xg, ws, nb, stream)
-        else:
-            nb = poetx_forward_q8_workspace_bytes(L, T, q8)
-            ws = self.workspace("fwd", nb, stream)
-            with torch.cuda.device(x.device):
+        with self._on(stream):
+            self._dequantize(stream)
+            L = self._abi()
+            q8 = self._q8(y, xg)
+            if q8 is None:
+                nb = poetx_forward_workspace_bytes(L, T)
+                ws = self.workspace("fwd", nb, stream)
+                poetx_forward(L, T, x, z, y, xg, ws, nb, stream)
+            else:
+                nb = poetx_forward_q8_workspace_bytes(L, T, q8)
+                ws = self.workspace("fwd", nb, stream)
                 poetx_forward_q8(L, T, x, z, None if save8 else y, None if save8 else xg, q8, ws, nb, stream)
         return z, (Saved(y, xg) if save else None)
 
@@ -297,7 +308,6 @@ class PoetxLinear:
         self._check_backward(T, x, saved, dz, dx if need_dx else None)
         _need(dqR, tuple(self.qR.shape), torch.float32, self.device, "dqR")
         _need(dqP, tuple(self.qP.shape), torch.float32, self.device, "dqP")
-        self._dequantize(stream)
         self._backward(poetx_backward, poetx_backward_q8, T, x, saved, dz, dx if need_dx else None, dqR, dqP, accumulate,
                        stream)
         return (dx if need_dx else None), dqR, dqP
@@ -318,24 +328,25 @@ class PoetxLinear:
         self._check_backward(T, x, saved, dz, dx if need_dx else None)
         _need(dGR, (self.m // self.b, self.b, self.b), torch.float32, self.device, "dGR")
         _need(dGP, (self.n // self.b, self.b, self.b), torch.float32, self.device, "dGP")
-        self._dequantize(stream)
         self._backward(poetx_backward_dG, poetx_backward_dG_q8, T, x, saved, dz, dx if need_dx else None, dGR, dGP,
                        accumulate, stream)
         return dx if need_dx else None
 
     def _backward(self, call, call_q8, T: int, x, saved: "Saved", dz, dx, gR, gP, accumulate: bool, stream) -> None:
-        L = self._abi()
-        q8 = self._q8(saved.y, saved.xg)
-        y = None if isinstance(saved.y, Checkpoint) else saved.y
-        xg = None if isinstance(saved.xg, Checkpoint) else saved.xg
-        if q8 is None:
-            nb = (poetx_backward_workspace_bytes if y is not None else poetx_backward_recompute_workspace_bytes)(L, T)
-            ws = self.workspace("bwd", nb, stream)
-            call(L, T, x, y, xg, dz, dx, gR, gP, int(accumulate), ws, nb, stream)
-        else:
-            nb = poetx_backward_q8_workspace_bytes(L, T, int(y is not None), q8)
-            ws = self.workspace("bwd", nb, stream)
-            with torch.cuda.device(dz.device):
+        with self._on(stream):
+            self._dequantize(stream)
+            L = self._abi()
+            q8 = self._q8(saved.y, saved.xg)
+            y = None if isinstance(saved.y, Checkpoint) else saved.y
+            xg = None if isinstance(saved.xg, Checkpoint) else saved.xg
+            if q8 is None:
+                nb = (poetx_backward_workspace_bytes if y is not None else
+                      poetx_backward_recompute_workspace_bytes)(L, T)
+                ws = self.workspace("bwd", nb, stream)
+                call(L, T, x, y, xg, dz, dx, gR, gP, int(accumulate), ws, nb, stream)
+            else:
+                nb = poetx_backward_q8_workspace_bytes(L, T, int(y is not None), q8)
+                ws = self.workspace("bwd", nb, stream)
                 call_q8(L, T, x, y, xg, q8, dz, dx, gR, gP, int(accumulate), ws, nb, stream)
 
     def _check_backward(self, T: int, x, saved: "Saved", dz, dx) -> None:
@@ -358,11 +369,11 @@ class PoetxLinear:
         q = 0 and G = I afterwards.  The merged weight of a quantized layer is
         quantized again, into the same codes and scales."""
         self._need_weight("merge")
-        self._dequantize(stream)
-        L = self.abi()
-        nb = poetx_merge_workspace_bytes(L)
-        ws = self.workspace("merge", nb, stream)
-        with _on(stream, self.device):
+        with self._on(stream):
+            self._dequantize(stream)
+            L = self.abi()
+            nb = poetx_merge_workspace_bytes(L)
+            ws = self.workspace("merge", nb, stream)
             W_out = torch.empty_like(self.W)
             newR = new_permR.to(device=self.device, dtype=torch.int32).contiguous()
             newP = new_permP.to(device=self.device, dtype=torch.int32).contiguous()
@@ -396,7 +407,7 @@ class Int8Linear:
         self.Wq = torch.empty((self.n, self.m), dtype=torch.int8, device=W.device)
         self.wscale = torch.empty(self.n, dtype=torch.float32, device=W.device)
         code = next(k for k, v in _TORCH_DTYPE.items() if v == W.dtype)
-        with torch.cuda.device(W.device):
+        with _on(stream, W.device):
             poetx_weight_quantize(self.n, self.m, W, code, self.Wq, self.wscale, stream)
 
     @classmethod
@@ -409,7 +420,7 @@ class Int8Linear:
         if there != here:
             there.wait_stream(here)
         # every copy and temporary belongs to the stream that uses it
-        with torch.cuda.device(layer.device), torch.cuda.stream(there):
+        with _on(there, layer.device):
             layer._dequantize(there)
             # merge a copy of the layer's state into the natural order (identity permutations)
             keep = [t.clone() for t in (layer.qR, layer.qP, layer.GR, layer.GP)]
@@ -478,8 +489,9 @@ class LayerGroup:
             raise RuntimeError("flatten_params() first")
         _need(grad, tuple(self.q.shape), torch.float32, self.q.device, "grad")
         self.steps += 1
-        poetx_adamw_step(self.q.numel(), self.q, grad, self.m1, self.m2, lr, beta1, beta2, eps, weight_decay,
-                         self.steps, stream)
+        with _on(stream, self.q.device):
+            poetx_adamw_step(self.q.numel(), self.q, grad, self.m1, self.m2, lr, beta1, beta2, eps, weight_decay,
+                             self.steps, stream)
         self.build(stream)
 
     def dG_buffer(self) -> torch.Tensor:
@@ -507,12 +519,14 @@ class LayerGroup:
         nblk = sum(L.m // L.b + L.n // L.b for L in self.layers)
         _need(dG, (nblk, L0.b, L0.b), torch.float32, self.q.device, "dG")
         _need(dq, tuple(self.q.shape), torch.float32, self.q.device, "dq")
-        nb = poetx_cnp_workspace_bytes(nblk, L0.b, L0.dtype)
-        ws = _workspace(self._ws, "bwd", nb, L0.device, stream)
-        poetx_cnp_backward(nblk, L0.b, self.q, dG, dq, int(accumulate), L0.dtype, ws, nb, stream)
+        with _on(stream, self.q.device):
+            nb = poetx_cnp_workspace_bytes(nblk, L0.b, L0.dtype)
+            ws = _workspace(self._ws, "bwd", nb, L0.device, stream)
+            poetx_cnp_backward(nblk, L0.b, self.q, dG, dq, int(accumulate), L0.dtype, ws, nb, stream)
 
     def build(self, stream=None) -> None:
-        abis = [L._abi() for L in self.layers]
-        nb = poetx_layers_cnp_workspace_bytes(abis)
-        ws = _workspace(self._ws, "build", nb, self.layers[0].device, stream)
-        poetx_layers_cnp_build(abis, ws, nb, stream)
+        with self.layers[0]._on(stream):
+            abis = [L._abi() for L in self.layers]
+            nb = poetx_layers_cnp_workspace_bytes(abis)
+            ws = _workspace(self._ws, "build", nb, self.layers[0].device, stream)
+            poetx_layers_cnp_build(abis, ws, nb, stream)

@@ -47,6 +47,7 @@ class Streams:
             return t
 
         monkeypatch.setattr(torch.cuda, "stream", On)
+        monkeypatch.setattr(torch.cuda, "device", lambda d: On(None))
         monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing)
         monkeypatch.setattr(torch, "empty", made)
         monkeypatch.setattr(layer_py, "_torch_stream", lambda s, device: s, raising=False)
@@ -85,3 +86,58 @@ def test_every_call_asks_for_scratch_on_its_stream(monkeypatch):
     group.build(stream="side")
     group.cnp_backward(dG, torch.zeros_like(group.q), stream="side")
     assert asked == [(k, "side") for k in ("fwd", "bwd", "bwd", "cnp", "merge", "build", "bwd")]
+
+
+def test_the_context_of_a_call_switches_to_its_device_and_stream(monkeypatch):
+    s, seen = object(), []
+    monkeypatch.setattr(layer_py, "_torch_stream", lambda stream, device: stream)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: seen.append(("device", d)))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: seen.append(("stream", s)))   # (switches the device as well)
+    for stream in (None, s):
+        layer_py._on(stream, torch.device("cuda", 1))
+    layer_py._on(None, torch.device("cpu"))
+    assert seen == [("device", torch.device("cuda", 1)), ("stream", s)]
+
+
+@pytest.mark.parametrize("form", ["full", "codes", "int8_product"])
+def test_every_call_of_a_layer_runs_on_its_device(monkeypatch, form):
+    # a layer on another device than the current one: each C call, the expansion of a quantized weight among
+    # them, is made inside the context of the layer's device
+    inside, calls = [], []
+
+    class On:
+        def __init__(on, stream, device):
+            on.at = (stream, device.type)
+
+        def __enter__(on):
+            inside.append(on.at)
+
+        def __exit__(on, *a):
+            inside.pop()
+
+    monkeypatch.setattr(layer_py, "_on", On)
+    names = [n for n in dir(layer_py) if n.startswith("poetx_") and not n.endswith("_bytes")]
+    for name in names:
+        monkeypatch.setattr(layer_py, name, lambda *a, name=name: calls.append((name, inside[-1] if inside else None)))
+    L = px.PoetxLinear(128, 192, 64, px.POETX_BF16, device="cpu")
+    group = px.LayerGroup([L])
+    q = group.flatten_params()
+    dG = group.dG_buffer()
+    x, dz = torch.zeros(4, 128, dtype=BF), torch.zeros(4, 192, dtype=BF)
+    if form != "full":
+        L.quantize_weight(stream="s", int8_product=form == "int8_product")
+    for save8 in (False, True):
+        _, saved = L.forward(x, save8=save8, stream="s")
+        L.backward(x, saved, dz, stream="s")
+        L.backward_dG(x, saved, dz, *group.dG_views(dG)[0], stream="s")
+    if form != "int8_product":
+        L.export_weight(stream="s")
+        L.merge(L.permR, L.permP, stream="s")
+    group.cnp_backward(dG, torch.zeros_like(q), stream="s")
+    group.optimizer_step(torch.zeros_like(q), 1e-3, stream="s")
+    L.load(L.W.new_zeros(192, 128, dtype=BF), L.permR, L.permP, L.qR, L.qP, stream="s")
+    assert {at for _, at in calls} == {("s", "cpu")}
+    want = {"poetx_forward_q8", "poetx_backward_q8", "poetx_backward_dG_q8", "poetx_cnp_backward", "poetx_adamw_step",
+            "poetx_layers_cnp_build", "poetx_frame_import", "poetx_layer_cnp_build"}
+    want |= {"full": {"poetx_merge"}, "codes": {"poetx_merge", "poetx_weight_dequantize"}, "int8_product": set()}[form]
+    assert want <= {name for name, _ in calls}
