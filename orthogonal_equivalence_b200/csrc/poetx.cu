@@ -1466,9 +1466,19 @@ int block_f32_splits(int nblk, int b, int64_t T) {
   return s < 1 ? 1 : s > 32 ? 32 : static_cast<int>(s);
 }
 
+// Other bf16 blocks: the layer's own splits, but of SPLIT_TOKENS at most, for
+// the same reason (bdg8.cuh).  16384 x 8192 in 8 splits and in the one that
+// dg_splits takes: error of dG against 64 bits 4e-7 and 7e-6; b = 64 312 and
+// 294 us, b = 512 388 and 336 us.
+int gemm_block_splits(int nblk, int b, int64_t T) {
+  const int64_t least = (T + bdg8::SPLIT_TOKENS - 1) / bdg8::SPLIT_TOKENS;
+  const int s = dg_splits(nblk, b, T, POETX_BF16);
+  return s < least ? static_cast<int>(least) : s;
+}
+
 int block_backward_splits(int64_t T, int32_t d, int32_t b, int32_t dtype) {
   if (dtype == POETX_FP32) return block_f32_splits(d / b, b, T);
-  return use_pair_bdg8(b, dtype) ? bdg8_splits(d / b, T) : dg_splits(d / b, b, T, dtype);
+  return use_pair_bdg8(b, dtype) ? bdg8_splits(d / b, T) : gemm_block_splits(d / b, b, T);
 }
 
 cudaError_t launch_block_f32(const void* D, const int8_t* codes, const uint8_t* exps, const void* G, void* O,

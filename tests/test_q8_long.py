@@ -1,0 +1,65 @@
+"""The 8-bit operators over many rows: sums over long ranges of tokens, and
+blocks of threads that take several rows or tiles in turn.
+
+u24 = 2^-24 is half a step of fp32.  The tensor core adds the 16 tokens of an
+instruction to its fp32 sum at a time and cuts off what the addition shifts
+out: the terms' and the sum's own step, two whole steps 2^-23 of the sum so far
+at most."""
+import pytest
+import torch
+
+import orthogonal_equivalence_b200 as px
+from orthogonal_equivalence_b200 import build as pbuild
+
+BF, F32 = torch.bfloat16, torch.float32
+U24 = 2.0 ** -24
+SPLIT = 2048 + 256      # most tokens of one sum: about 2048, to whole tiles
+
+
+@pytest.fixture(scope="module")
+def gpu():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    pbuild.build()
+    px.lib()
+    px.poetx_device_error()
+    yield
+    torch.cuda.synchronize()
+    assert px.poetx_device_error() == 0
+
+
+def rnd(seed, *shape, dtype=F32, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+# ---------------------------------------------------------------- token sums
+@pytest.mark.parametrize("T", [2049, 16384, 70001])
+@pytest.mark.parametrize("b", [64, 128, 256, 512])
+def test_partial_sums_for_every_2048_tokens(b, T):
+    pbuild.build()
+    d = 8192
+    expanded = 0 if b == 256 else 2 * T * d     # X in bf16, where no kernel reads the codes
+    sums = -(-T // 2048) * 4 * d * b
+    assert px.poetx_block_backward_workspace_bytes(T, d, b, px.POETX_BF16) >= expanded + sums
+    # the layer's backward from checkpoints sums the same way
+    L = px.poetx_layer(d, d, b, px.POETX_BF16, 16, 16, 16, 16, 16, 16, 16, 0)
+    kept = px.poetx_q8(None, None, 16, 16, 16, 16)
+    more = px.poetx_backward_q8_workspace_bytes(L, T, 0, kept) - px.poetx_backward_q8_workspace_bytes(L, T, 1, px.poetx_q8())
+    assert more >= expanded + 2 * sums
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,d", [(16384, 8192), (5000, 8192), (16384, 1024)])
+@pytest.mark.parametrize("b", [64, 128, 256, 512])
+def test_long_token_sums(gpu, b, T, d):
+    # terms of one sign: what an addition cuts off adds up.  A sum of S tokens is S / 16 additions to a sum that
+    # grows evenly, half of the last on average, so it loses (S / 16 + 1) 2^-23 of itself at most; then the splits'
+    # sums are added, each addition rounded.
+    x, D = rnd(1, T, d, dtype=BF).abs(), rnd(2, T, d, dtype=BF).abs()
+    c = px.checkpoint_save(x)
+    _, dG = px.block_backward(c, D, rnd(3, d // b, b, b, dtype=BF), need_o=False)
+    X = px.checkpoint_load(c, F32)
+    bound = (SPLIT / 16 + 1) * 2 * U24 + (-(-T // 1024) + 1) * U24
+    for j in range(0, d // b, max(1, d // b // 8)):
+        want = X[:, j * b:(j + 1) * b].double().t() @ D[:, j * b:(j + 1) * b].double()
+        assert ((dG[j].double() - want).abs() <= bound * want).all()
