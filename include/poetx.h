@@ -260,7 +260,8 @@ poetx_status poetx_selftest_wait_timeout(uint32_t limit_us, unsigned long long* 
  * base weight is kept quantized and dequantized at run time.  The pages fix no
  * format; the reading here is int8, symmetric, one fp32 scale per row of the
  * stored [n][m] weight (per output feature): scale = max|row| / 127, code =
- * round-half-even(w / scale) clamped to [-127, 127] (fp32 arithmetic).
+ * round-half-even(w / scale) clamped to [-127, 127] (fp32 arithmetic).  A row
+ * that holds an infinity or a NaN gets codes 0 and scale NaN.
  * quantize: W [n][m] (dtype) -> Wq [n][m] int8 + scale [n] fp32.
  * dequantize: w = code * scale (fp32 product) rounded once to dtype, into W;
  * run it into a scratch weight before poetx_forward / poetx_backward. */

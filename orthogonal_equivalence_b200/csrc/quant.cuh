@@ -21,25 +21,28 @@ __device__ __forceinline__ float load_f32<__nv_bfloat16>(const __nv_bfloat16* p,
   return __bfloat162float(p[i]);
 }
 
-// One block per row: absmax by a block reduction, then the codes.
+// One block per row: absmax by a block reduction, then the codes.  A row that
+// holds an infinity or a NaN gets codes 0 and scale NaN, as in q8.cuh: the
+// maximum is taken over the magnitudes' bits, which keeps a NaN above all else.
 template <typename T>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const T* __restrict__ W, int64_t rows, int cols,
                                                             int8_t* __restrict__ Wq, float* __restrict__ scale) {
-  __shared__ float red[8];
+  __shared__ uint32_t red[8];
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
     const T* w = W + r * cols;
-    float amax = 0.f;
-    for (int c = threadIdx.x; c < cols; c += blockDim.x) amax = fmaxf(amax, fabsf(load_f32(w, c)));
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
+    uint32_t top = 0;
+    for (int c = threadIdx.x; c < cols; c += blockDim.x) top = max(top, __float_as_uint(load_f32(w, c)) & 0x7fffffffu);
+    top = __reduce_max_sync(0xffffffffu, top);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = top;
     __syncthreads();
     if (threadIdx.x < 32) {
-      float v = threadIdx.x < (blockDim.x >> 5) ? red[threadIdx.x] : 0.f;
-      for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+      const uint32_t v = __reduce_max_sync(0xffffffffu, threadIdx.x < (blockDim.x >> 5) ? red[threadIdx.x] : 0u);
       if (threadIdx.x == 0) red[0] = v;
     }
     __syncthreads();
-    const float s = red[0] / 127.f;
+    const float amax = __uint_as_float(red[0]);
+    const bool finite = amax <= 3.402823466e38f;
+    const float s = finite ? amax / 127.f : __uint_as_float(0x7fffffffu);
     if (threadIdx.x == 0) scale[r] = s;
     for (int c = threadIdx.x; c < cols; c += blockDim.x) {
       float q = 0.f;

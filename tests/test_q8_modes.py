@@ -245,3 +245,48 @@ def test_load_merge_and_quantize_on_another_stream():
         same = torch.equal(z, want), torch.equal(z8, want8), torch.equal(L.Wq, full.Wq)
     assert same == (True, True, True)
     torch.cuda.synchronize()
+
+
+# ---------------------------------------------------------------- weights that are not finite
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("m", [1, 33, 512, 1000])
+def test_a_weight_that_is_not_finite_stays_visible(m, dtype):
+    n = 9
+    W = rnd(1, n, m, dtype=dtype)
+    clean = px.Int8Linear(W)
+    bad = W.clone()
+    for row, v in ((1, float("nan")), (3, float("inf")), (4, -float("inf")), (6, -float("nan"))):
+        bad[row, (row * 7) % m] = v
+    bad[7, 0], bad[7, m - 1] = float("inf"), float("nan")
+    rows = torch.tensor([1, 3, 4, 6, 7])
+    lin = px.Int8Linear(bad)
+    keep = torch.ones(n, dtype=torch.bool)
+    keep[rows] = False
+    assert torch.equal(lin.Wq[keep], clean.Wq[keep]) and torch.equal(lin.wscale[keep], clean.wscale[keep])
+    assert torch.isnan(lin.wscale[rows]).all() and not lin.Wq[rows].any()
+    x = rnd(2, 5, m, dtype=dtype)
+    z = lin.forward(x)
+    assert torch.isnan(z[:, rows]).all() and torch.equal(z[:, keep], clean.forward(x)[:, keep])
+    # the token's quantiser marks the same rows
+    q, s = px.quantize_rows(bad)
+    assert torch.equal(torch.isnan(s), torch.isnan(lin.wscale)) and not q[rows].any()
+
+
+@pytest.mark.parametrize("int8_product", [False, True])
+def test_a_layer_whose_weight_is_not_finite(int8_product):
+    st = state(256, 512, 256, BF, 0)
+    st[0][5, 7] = float("nan")
+    L = layer(256, 512, 256, BF, (*st[:3], torch.zeros_like(st[3]), torch.zeros_like(st[4])))   # G = I
+    L.quantize_weight(int8_product=int8_product)
+    z = L.forward(rnd(1, 20, 256, dtype=BF))[0]
+    assert torch.isnan(z[:, 5]).all()
+
+
+def test_the_largest_and_smallest_weights():
+    # rows at both ends of the range keep the codes the formula gives
+    big, tiny = 3.4028234663852886e38, 2.0 ** -149
+    W = torch.tensor([[big, -big, big / 2, 0.0], [127 * tiny, -64 * tiny, 1 * tiny, 0.0], [0.0] * 4], device="cuda")
+    lin = px.Int8Linear(W)
+    # (the scale is rounded up from big / 127, by 5.6e-8 of it, so big / 2 lies below the border 63.5: 63.499996)
+    assert lin.Wq.tolist() == [[127, -127, 63, 0], [127, -64, 1, 0], [0] * 4]
+    assert lin.wscale.tolist() == [(W[0, 0] / torch.tensor(127.0, device="cuda")).item(), tiny, 0.0]
