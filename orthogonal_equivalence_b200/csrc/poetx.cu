@@ -1022,7 +1022,7 @@ namespace {
 template <typename T, bool SAVE, typename F>
 cudaError_t with_chunks(int64_t rows, int d, int device, F f) {
   auto grid = [&](int cols) {
-    const int gx = (d + 4 * cols - 1) / (4 * cols);
+    const int gx = (d - 1) / (4 * cols) + 1;  // (a weight's rows may be as long as an int)
     int64_t gy = (int64_t(sm_count(device)) * 64 + gx - 1) / gx;  // four blocks' worth for each of the 16 a SM holds
     if (gy > rows) gy = rows;
     return dim3(gx, static_cast<unsigned>(gy > 65535 ? 65535 : gy));

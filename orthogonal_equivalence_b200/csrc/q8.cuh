@@ -847,7 +847,7 @@ __global__ void __launch_bounds__(128) expand_kernel(const int8_t* __restrict__ 
                                                      const float* __restrict__ scale, int64_t rows, int d,
                                                      T* __restrict__ x) {
   const int lane = threadIdx.x & 31;
-  const int ng = (d + GROUP - 1) / GROUP;
+  const int ng = (d - 1) / GROUP + 1;
   const int c0 = (blockIdx.x * 4 + (threadIdx.x >> 5)) * chunk_cols<N>;
   if (c0 >= d) return;
   for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {

@@ -63,3 +63,15 @@ def test_long_token_sums(gpu, b, T, d):
     for j in range(0, d // b, max(1, d // b // 8)):
         want = X[:, j * b:(j + 1) * b].double().t() @ D[:, j * b:(j + 1) * b].double()
         assert ((dG[j].double() - want).abs() <= bound * want).all()
+
+
+# ---------------------------------------------------------------- the longest rows
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [2 ** 31 - 16, 2 ** 31 - 1])
+def test_a_row_as_long_as_an_int(gpu, d):
+    codes = torch.arange(-128, 128, device="cuda").to(torch.int8).repeat(d // 256 + 1)[:d].view(1, d)
+    scale = torch.tensor([0.37], device="cuda")
+    w = px.dequantize_rows(codes, scale, BF)
+    one = (torch.arange(-128, 128, device="cuda").float() * scale).to(BF)
+    assert torch.equal(w[0, :d // 256 * 256].view(-1, 256), one.expand(d // 256, 256))
+    assert torch.equal(w[0, d // 256 * 256:], one[:d % 256])
