@@ -64,10 +64,21 @@ def build_tensors(force: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
-    build_tensors(force)
+    """The library, then the extension; the library alone, which needs nothing
+    but nvcc, where torch is not installed."""
     lib = LIB_DEBUG if debug else LIB
-    if not force and not needs_build(lib):
+    if force or needs_build(lib):
+        build_library(lib, verbose, debug)
+    try:
+        import torch  # noqa: F401
+    except ImportError as e:
+        sys.stderr.write(f"{os.path.basename(TENSORS)} (the torch functions) not built: {e}\n")
         return lib
+    build_tensors(force)
+    return lib
+
+
+def build_library(lib: str, verbose: bool, debug: bool) -> None:
     cmd = [nvcc(), "-std=c++17", "-O3", "-lineinfo", "-gencode", "arch=compute_100a,code=sm_100a",
            "-shared", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include"), "-I", CSRC,
            "-o", lib + ".tmp"] + [os.path.join(CSRC, s) for s in SOURCES] + ["-lcudart"]
@@ -83,7 +94,6 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     if verbose:
         sys.stderr.write(r.stderr)
     os.replace(lib + ".tmp", lib)
-    return lib
 
 
 if __name__ == "__main__":
