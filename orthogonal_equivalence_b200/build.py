@@ -39,10 +39,24 @@ def needs_build(lib: str = LIB) -> bool:
     return any(os.path.getmtime(d) > t for d in deps() if os.path.exists(d))
 
 
+def built_for() -> bytes:
+    """What an extension is compiled against, as _tensors.so holds it."""
+    import torch
+    return f"poetx built for torch {torch.__version__}, {sys.implementation.cache_tag};".encode()
+
+
+def tensors_up_to_date(src) -> bool:
+    if not os.path.exists(TENSORS) or os.path.getmtime(TENSORS) < max(os.path.getmtime(f) for f in src):
+        return False
+    with open(TENSORS, "rb") as f:
+        return built_for() in f.read()
+
+
 def build_tensors(force: bool = False) -> str:
-    """The extension of csrc/tensors.cpp, compiled against the installed torch."""
+    """The extension of csrc/tensors.cpp, compiled against the installed torch
+    (again when that or Python has changed)."""
     src = [os.path.join(CSRC, "tensors.cpp"), os.path.join(ROOT, "include", "poetx.h")]
-    if not force and os.path.exists(TENSORS) and os.path.getmtime(TENSORS) >= max(os.path.getmtime(f) for f in src):
+    if not force and tensors_up_to_date(src):
         return TENSORS
     import sysconfig
 
@@ -51,7 +65,8 @@ def build_tensors(force: bool = False) -> str:
     cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
     tmp = f"{TENSORS}.{os.getpid()}.tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(ROOT, "include"),
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DPOETX_BUILT_FOR="{built_for().decode()}"', "-I", os.path.join(ROOT, "include"),
            "-I", os.path.join(at, "include"), "-I", os.path.join(at, "include", "torch", "csrc", "api", "include"),
            "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"), src[0], "-o", tmp,
            "-L", os.path.join(at, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python"]

@@ -420,4 +420,7 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", "Calls of libpoetx on t
 
 }  // namespace
 
+// What this file was compiled against; build.py looks for it in the built file.
+extern "C" __attribute__((used, visibility("default"))) const char poetx_tensors_built_for[] = POETX_BUILT_FOR;
+
 PyMODINIT_FUNC PyInit__tensors(void) { return PyModule_Create(&module); }

@@ -53,3 +53,17 @@ def test_an_extension_that_does_not_compile_leaves_the_library(compilers, monkey
     with pytest.raises(RuntimeError, match="_tensors.so"):
         pbuild.build()
     assert os.path.exists(pbuild.LIB)
+
+
+def test_the_extension_follows_torch_and_python(compilers, monkeypatch):
+    import torch
+    pbuild.build_tensors()
+    pbuild.build_tensors()
+    assert compilers == ["_tensors"]
+    monkeypatch.setattr(torch, "__version__", "0.0.1+other")
+    pbuild.build_tensors()
+    pbuild.build_tensors()
+    assert compilers == ["_tensors"] * 2
+    monkeypatch.setattr(sys.implementation, "cache_tag", "cpython-399")
+    pbuild.build_tensors()
+    assert compilers == ["_tensors"] * 3
