@@ -75,3 +75,58 @@ def test_a_row_as_long_as_an_int(gpu, d):
     one = (torch.arange(-128, 128, device="cuda").float() * scale).to(BF)
     assert torch.equal(w[0, :d // 256 * 256].view(-1, 256), one.expand(d // 256, 256))
     assert torch.equal(w[0, d // 256 * 256:], one[:d % 256])
+
+
+# ---------------------------------------------------------------- several rows or tiles in turn
+# More rows than the grid has blocks (at most 16 blocks a SM), so that a block loads its next row while it
+# works on one and keeps its share of dgamma over all of them: every register shape of the row kernels, with
+# whole rows and cut ones, bf16 and fp32.
+TURNS = [(3000, 512), (2500, 1024), (3000, 2048), (1500, 4096), (1300, 3584), (900, 5120), (1200, 7168), (700, 8192),
+         (700, 14336), (500, 16384), (5001, 264), (2600, 648)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,d", TURNS)
+def test_blocks_that_take_several_rows(gpu, T, d, dtype):
+    from test_q8_gpu import test_quantize_rows, test_rmsnorm_backward, test_rmsnorm_quantize
+    test_quantize_rows(T, d, dtype)
+    for residual in (False, True):
+        test_rmsnorm_quantize(T, d, residual, dtype)
+        test_rmsnorm_backward(T, d, residual, dtype)
+
+
+# More items (block, token split) than the 74 pairs of SMs, with values everywhere: a pair's second item takes over
+# the accumulators, the resident G and every ring in mid-phase; and other blocks beside them.
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,d,b", [(16384, 2304, 256), (5000, 8192, 256), (300, 38400, 256), (1, 25600, 256), (16384, 4096, 256),
+                                   (12345, 5120, 512), (9000, 1920, 64), (7001, 2688, 128)])
+def test_blocks_of_more_items_than_pairs(gpu, T, d, b):
+    D, G = rnd(11, T, d, dtype=BF), rnd(12, d // b, b, b, dtype=BF, scale=0.3)
+    c = px.checkpoint_save(rnd(10, T, d, dtype=BF))
+    O, dG = px.block_backward(c, D, G)
+    none, alone = px.block_backward(c, D, G, need_o=False)
+    assert none is None and torch.equal(alone, dG)
+    X = px.checkpoint_load(c, F32)
+    terms = min(T, SPLIT) + -(-T // 1024) + 34      # of a sum: a split's tokens, then the splits
+    for j in range(d // b):
+        at = slice(j * b, (j + 1) * b)
+        Dj, Gj, Xj = D[:, at].double(), G[j].double(), X[:, at].double()
+        want, size = Dj @ Gj.t(), Dj.abs() @ Gj.abs().t()
+        # fp32 accumulation, up to a whole step cut off a term; O is rounded to bf16
+        assert ((O[:, at].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2 * (b + 2) * U24 * size).all(), ("O", j)
+        want, size = Xj.t() @ Dj, Xj.abs().t() @ Dj.abs()
+        assert ((dG[j].double() - want).abs() <= 2 * terms * U24 * size).all(), ("dG", j)
+
+
+# Tiles of 128 tokens by the weight's rows: one wave of them for up to 128 tokens of a wide weight, and a long K
+# split in two; and many tiles on each pair.
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,m,n", [(100, 256, 20000), (128, 512, 19201), (512, 8192, 4096), (500, 9000, 4000),
+                                   (3000, 384, 6000), (9001, 128, 4096)])
+def test_wide_and_many_int8_tiles(gpu, T, m, n, dtype):
+    from test_q8_gpu import test_matmul_int8, test_matmul_int8_grad
+    test_matmul_int8(T, m, n, dtype)
+    test_matmul_int8_grad(T, n, m, dtype)      # the same tiles, the weight's rows as K
+    test_matmul_int8_grad(T, m, n, dtype)
