@@ -17,9 +17,9 @@
 // of 16 KB units for converted X, and the epilogue's boxes.
 //
 // Token sums: the tensor core cuts off rather than rounds what an addition
-// shifts out, which biases a sum of many terms towards zero (1.2e-6 of dG over
-// four splits of 16384 tokens, 1e-7 over splits of 2048), so a split takes
-// about 2048 tokens at most.
+// shifts out, which biases a sum of many terms towards zero (dG of 16384 tokens,
+// normal values: off by 7.0e-6 as one sum, 2.8e-6 as two, 1.1e-6 as four, 4e-7 as
+// eight or nine), so a split takes about 2048 tokens at most.
 //
 //   warp 0: TMA producer (both CTAs)
 //   warp 1: TMEM owner (both CTAs) and MMA issuer (leader only)
@@ -40,11 +40,13 @@
 // released, and the next one loaded, before the last tile's dG; an item's first
 // O is computed while the dG before it is written.
 //
-// 16384 x 4096 takes 85 us with the sum of the nine splits, 54 us without
-// O (53 and 32 us at the copy rate).  Neither HBM (50%) nor the tensor pipe (48%)
-// is the bound, nor the conversion (left out: 80 and 52 us; with four warps 9 us
-// more): the O tiles' way through registers and boxes and the ends of the items
-// are; deeper rings of any of the three operands change nothing.
+// 16384 x 4096 takes 87 us with the sum of the nine splits and 58 us without O
+// (53 and 32 us at the copy rate) at 1965 MHz, and 98 to 103 us back to back for
+// seconds, when the power cap (990 W drawn, sw_power_cap) holds the SMs at 1590
+// MHz.  Neither HBM (50%) nor the tensor pipe (48%) is the bound, nor the conversion
+// (left out: 5 us less; with four warps 9 us more): the O tiles' way through
+// registers and boxes and the ends of the items are; deeper rings of any of the
+// three operands change nothing.
 // Every wait is bounded (ptx.cuh).  No load uses multicast.
 #pragma once
 

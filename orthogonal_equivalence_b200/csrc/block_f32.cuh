@@ -12,8 +12,8 @@
 // decoded on its way to shared memory.  Rows of either operand are read along
 // themselves, 16 bytes a thread where b is a multiple of four (VEC).
 //
-// 16384 x 2048, b = 64: 272 us, 16351 x 1920, b = 96: 454 us (123 and 172 us at
-// 70 TFLOP/s), bound by the shared reads.  8 x 8 sums a thread spill (O 17 us less
+// 16384 x 2048, b = 64: 272-280 us, 16351 x 1920, b = 96: 454-464 us (123 and 172 us
+// at 70 TFLOP/s), bound by the shared reads.  8 x 8 sums a thread spill (O 17 us less
 // there, dG 20 us more, and 300 x 512 11.4 instead of 8.3 us).
 #pragma once
 

@@ -127,8 +127,8 @@ struct PairParams {
 // takes 165 us (72 at the copy rate) with eight warps whose scales are loaded a
 // block of columns ahead, 228 with four, and 430 with four that wait for them.
 // Bound by the tensor pipe and the power cap: 16384 x 4096 -> 14336 takes 619 us
-// (3.1 POP/s, the pipe 84% active) in a short run and 730 in a long one, the
-// gradient's product 8192 x 14336 -> 4096 294 us (91%).  Asking L2 for operands
+// (3.1 POP/s, the pipe 84% active) in a short run and 690 to 730 in a long one,
+// the gradient's product 8192 x 14336 -> 4096 294 us (91%).  Asking L2 for operands
 // ahead of the stages costs 10% (the way from L2 to the SMs is nearly full too).
 template <typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
@@ -363,9 +363,10 @@ __device__ __forceinline__ void grid_launch() { asm volatile("griddepcontrol.lau
 
 // Grid (S, ceil(N / 128), ceil(T / nt)), clusters of the S CTAs of one tile.
 // CTA s takes the K blocks [s nkb / S, (s + 1) nkb / S), S <= nkb.  For a few
-// tokens the weight's bytes bound it: 1 x 4096 -> 14336 takes 13.2 us (9.0 at
-// the copy rate), 48 x 14336 -> 4096 16.4 us; what is left over is the launch,
-// the first loads' way and the sums' exchange.  With more tokens the epilogue
+// tokens the weight's bytes bound it: 1 x 4096 -> 14336 takes 12.7 us in a graph
+// and 13.3 called one after the other (9.0 at the copy rate), 48 x 14336 -> 4096
+// 14.0 and 15.4 (9.2); what is left over is the launch, the first loads' way and
+// the sums' exchange.  With more tokens the epilogue
 // (one weight row a thread) counts, which is why the tiles stay narrow.
 template <typename T>
 __global__ void __launch_bounds__(NUM_THREADS)

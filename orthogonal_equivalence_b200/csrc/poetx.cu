@@ -1072,7 +1072,9 @@ poetx_status check_opt(const void* p) { return aligned16(p) ? POETX_OK : POETX_E
 // not do); wider rows (K = 0) are read twice.  K trades the fixed work of a row
 // (reduction, scale: ~150 instructions a warp) against registers; measured at
 // 16384 x 4096 bf16 when it was chosen, K = 1, 2, 4: rows to int8 50, 51, 45 us,
-// norm 117, 90, 90 us, its backward 92, 88, 150 us.
+// norm 117, 90, 90 us, its backward 92, 88, 150 us.  (The fp32 norm backward takes
+// V = 1 up to 7168, 2 * 8 * kRowThreads, the widest row that V = 1 holds in
+// registers; beyond it both go through shared memory, where V = 2 is the faster.)
 constexpr int kMaxShifted = 24576;
 struct RowShape {
   int V, K, threads;

@@ -24,7 +24,13 @@
 namespace poetx {
 namespace q8 {
 
-constexpr int kRowThreads = 448;   // most threads of a row's block: two blocks of 72 registers fit a SM
+// Most threads of a row's block: two blocks of 72 registers fit a SM (rows to
+// int8, and the norm up to K = 2).  The norm's backward holds more (98 at K = 2,
+// 128 and spills at K = 4); it and the norm take rows of more than 7168 elements
+// as K = 4, one block a SM: 16384 x 8192 bf16 174 us for the norm and 221 for its
+// backward with dres (144 and 164 at the copy rate), where rows of 4096 are
+// within a sixth of it.
+constexpr int kRowThreads = 448;
 
 // ---------------------------------------------------------------- loads and stores
 // Eight elements of a row of d as loaded: consecutive ones from c (V = 8,
@@ -376,8 +382,10 @@ struct RowsParams {
 // registers, and loads its next row's before it works on this one.  K = 0:
 // rows too wide for registers are read a second time (h as written; each
 // thread rereads only what it wrote itself).  Bound by HBM for the norm (16384 x
-// 4096 bf16 with a residual: 81 us, 72 at the copy rate), by the way through a
-// row, loads - reduction - codes, for the rows alone (40 us of 31).
+// 4096 bf16 with a residual: 82 us, 72 at the copy rate; fp32 145 of 133), by the
+// way through a row, loads - reduction - codes, for the rows alone (43 us of 31;
+// fp32 55 of 51) and for the widest ones (4096 x 28672 bf16, read twice: 100 us of
+// 54, the norm 230 of 126).
 template <typename T, bool NORM, int V, int K, bool FULL>
 __global__ void __launch_bounds__(NORM && K == 2 && V == 8 ? 512 : kRowThreads, NORM && (K == 4 || V == 1) ? 1 : 2)
     rows_kernel(const RowsParams p) {
@@ -504,7 +512,10 @@ struct NormGradParams {
 // blockIdx.x + gridDim.x, ...; a thread keeps its columns' share of dgamma in
 // registers over all of them (K > 0) or in its own words of shared memory
 // (K = 0, any width), so the sum's order is fixed by the grid alone.  Bound by
-// HBM: 16384 x 4096 bf16 with dres 80 us, 82 at the copy rate.
+// HBM: 16384 x 4096 bf16 with dres 83 us (94 in a long run), 82 at the copy rate;
+// fp32 156 of 164.  Rows of more than 7168 elements do not fit two blocks a SM, and
+// fp32 ones go through shared memory: 8192 x 8192 118 us of 82, fp32 221 of 164;
+// 8192 x 14336 225 us of 144, fp32 430 of 287.
 template <typename T, int V, int K, bool FULL>
 __global__ void __launch_bounds__(kRowThreads) norm_grad_kernel(const NormGradParams p) {
   extern __shared__ __align__(16) float sm[];  // V = 2: gamma; K = 0: the share of dgamma behind it
@@ -766,8 +777,8 @@ __device__ __forceinline__ float code_value(const uint32_t* w, int i) {
 
 // The kernels below give a warp 32 * N columns of a row, N of them consecutive
 // to a lane (16 or 8 bf16, 8 or 4 fp32), so that a warp's accesses are whole
-// lines: at 16384 x 4096 bf16 saving takes 32 us and reading back 35 us (31 us
-// is the copy rate).  N = 1,
+// lines: at 16384 x 4096 bf16 saving takes 33 us and reading back 36 us (31 us
+// is the copy rate), fp32 53 and 66 (51).  N = 1,
 // for rows that are no whole vectors: a lane takes one column of each of eight
 // groups.  Chunks of rows are walked without a division by the grid's shape:
 // blockIdx.x and the warp give the chunk, blockIdx.y strides over the rows.
