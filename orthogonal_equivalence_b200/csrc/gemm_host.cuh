@@ -121,6 +121,8 @@ cudaError_t launch_tc_typed(const GemmDesc& g, cudaStream_t st, int device) {
   const int nkb = (g.K + C::CH - 1) / C::CH;
   const int kb_per = (nkb + g.splits - 1) / g.splits;
   p.k_per_split = kb_per * C::CH;
+  // a split without a K block would store what the accumulator held before
+  if (int64_t(g.splits - 1) * p.k_per_split >= g.K) return cudaErrorInvalidValue;
   p.tiles_m = (g.M + tc::BM - 1) / tc::BM;
   p.tiles_n = (g.N + BN - 1) / BN;
   p.a_mn = g.A.mn_major;

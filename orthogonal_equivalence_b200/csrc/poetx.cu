@@ -224,6 +224,16 @@ int dg_splits(int nblk, int b, int64_t T, int32_t dtype) {
   return static_cast<int>(s);
 }
 
+// The same for sums by the K-split GEMM on the tensor cores, whose splits take
+// equal numbers of 64-token steps: as many as get one (33 steps in 8 splits are 5
+// each, and the eighth would be left without any; its part of the sum would be
+// what the accumulator held before).
+int gemm_splits(int splits, int64_t T, int32_t dtype) {
+  if (!use_tc(dtype)) return splits;  // (FFMA: a split without tokens is zeros)
+  const int64_t steps = (T + 63) / 64, each = (steps + splits - 1) / splits;
+  return static_cast<int>((steps + each - 1) / each);
+}
+
 // Scratch of the CNP build (3 b x b arrays per block) and backward (11).
 size_t cnp_bwd_ws(int32_t nblk, int32_t b) {
   const size_t u = sizeof(float) * size_t(nblk) * b * b;
@@ -1475,7 +1485,7 @@ int block_f32_splits(int nblk, int b, int64_t T) {
 int gemm_block_splits(int nblk, int b, int64_t T) {
   const int64_t least = (T + bdg8::SPLIT_TOKENS - 1) / bdg8::SPLIT_TOKENS;
   const int s = dg_splits(nblk, b, T, POETX_BF16);
-  return s < least ? static_cast<int>(least) : s;
+  return gemm_splits(s < least ? static_cast<int>(least) : s, T, POETX_BF16);
 }
 
 int block_backward_splits(int64_t T, int32_t d, int32_t b, int32_t dtype) {
@@ -1992,8 +2002,14 @@ static poetx_status backward_impl(const poetx_layer* layer, int64_t T, const voi
   const bool tc_path = use_tc(L.dtype);
   const int64_t mx = L.m > L.n ? L.m : L.n;
   const size_t bb = size_t(L.b) * L.b;
-  const int sP = y8 ? block_backward_splits(T, L.n, L.b, L.dtype) : dg_splits(nP, L.b, T, L.dtype);
-  const int sR = xg8 ? block_backward_splits(T, L.m, L.b, L.dtype) : dg_splits(nR, L.b, T, L.dtype);
+  const bool fold_p = fold_p_into_weight(L, T), pair = use_pair_bdg(L);
+  // token splits of either side, by the kernel that sums it
+  auto splits = [&](bool ckpt, int32_t d, bool fused) {
+    if (ckpt) return block_backward_splits(T, d, L.b, L.dtype);
+    const int s = dg_splits(d / L.b, L.b, T, L.dtype);
+    return fused ? s : gemm_splits(s, T, L.dtype);
+  };
+  const int sP = splits(y8, L.n, pair && !fold_p), sR = splits(xg8, L.m, pair);
   Carver c(ws, ws_bytes);
   void* bufA = c.take<uint8_t>(es * T * mx);
   void* bufB = c.take<uint8_t>(es * T * mx);
@@ -2038,13 +2054,12 @@ static poetx_status backward_impl(const poetx_layer* layer, int64_t T, const voi
   // [n][m], one weight-sized pass) and dU = dV W_P below, so only the dG
   // product reads dV here.
   void* dY = bufB;
-  const bool fold_p = fold_p_into_weight(L, T);
   if (y8) {
     POETX_TRY(side_q8(L, T, L.n, q->y_codes, q->y_exps, dV, L.GP, dY, partP, sP, expanded, st, dev));
   } else if (fold_p) {
     POETX_CUDA(fold_p_rows(L, L.W, bufB, st, dev));
     PROFILED(ST_DG, st, POETX_CUDA(launch_gemm(blockgrad_desc(y_save, dV, et, T, L.n, L.b, sP, partP), tc_path, st, dev)));
-  } else if (use_pair_bdg(L)) {
+  } else if (pair) {
     PROFILED(ST_BDG, st, POETX_CUDA(launch_bdg(dV, y_save, L.GP, dY, partP, T, L.n, sP, st, dev)));
   } else {
     PROFILED(ST_BLOCKDIAG, st, POETX_CUDA(launch_gemm(blockdiag_desc(dV, et, T, L.n, L.b, L.GP, true, dY, et), tc_path, st, dev)));
@@ -2085,7 +2100,7 @@ static poetx_status backward_impl(const poetx_layer* layer, int64_t T, const voi
   void* dXg = bufB;
   if (xg8) {
     POETX_TRY(side_q8(L, T, L.m, q->xg_codes, q->xg_exps, dU, L.GR, dx ? dXg : nullptr, partR, sR, expanded, st, dev));
-  } else if (use_pair_bdg(L)) {
+  } else if (pair) {
     PROFILED(ST_BDG, st, POETX_CUDA(launch_bdg(dU, Xg, L.GR, dx ? dXg : nullptr, partR, T, L.m, sR, st, dev)));
   } else {
     if (dx) PROFILED(ST_BLOCKDIAG, st, POETX_CUDA(launch_gemm(blockdiag_desc(dU, et, T, L.m, L.b, L.GR, true, dXg, et), tc_path, st, dev)));
