@@ -194,3 +194,57 @@ def test_products_wait_for_what_comes_before_them():
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+# ---------------------------------------------------------------- the layer
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("dtype,m,n,b,T", [(BF, 512, 768, 256, 300), (BF, 192, 320, 64, 2100), (BF, 512, 1024, 512, 130), (F32, 40, 60, 20, 500),
+                                           (F32, 9, 15, 3, 70), (BF, 256, 256, 256, 1)])
+def test_a_layer_between_margins(dtype, m, n, b, T, i8):
+    # every form of what is kept: scratch of exactly the size asked for, its bytes read as NaN
+    pd, tri = DT[dtype], b * (b - 1) // 2
+    L = px.PoetxLinear(m, n, b, pd)
+    g = torch.Generator().manual_seed(1)
+    L.load(rnd(1, n, m, dtype=dtype) * 0.05, torch.randperm(m, generator=g).int().cuda(),
+           torch.randperm(n, generator=g).int().cuda(), rnd(2, m // b, tri) * 0.02, rnd(3, n // b, tri) * 0.02)
+    abi = L.abi()
+    wq = {}
+    if i8:
+        Wq, ws = torch.empty(n, m, dtype=I8, device="cuda"), torch.empty(n, device="cuda")
+        px.poetx_weight_quantize(n, m, L.W, pd, Wq, ws)
+        wq = {"Wq": Wq, "wscale": ws}
+    x, dz = rnd(4, T, m, dtype=dtype), rnd(5, T, n, dtype=dtype)
+
+    def run(A, exact, y, xg):
+        """z, what is kept and the gradients; y and xg: None, "full" or "codes"."""
+        out = A.out if A else lambda *shape, dtype: torch.empty(*shape, dtype=dtype, device="cuda")
+        take = A.like if A else lambda t: t
+
+        def scratch(nbytes):
+            nbytes += 0 if exact else 1 << 22
+            return out(nbytes, dtype=torch.uint8), nbytes
+
+        def keep(form, d):
+            return (out(T, d, dtype=dtype) if form == "full" else None,
+                    (out(T, d, dtype=I8), out(T, (d + 31) // 32, dtype=torch.uint8)) if form == "codes" else (None, None))
+
+        ys, yc = keep(y, n)
+        xs, xc = keep(xg, m)
+        q = px.make_q8(**wq, y_codes=yc[0], y_exps=yc[1], xg_codes=xc[0], xg_exps=xc[1])
+        z, dx = out(T, n, dtype=dtype), out(T, m, dtype=dtype)
+        ax, adz = take(x), take(dz)
+        px.poetx_forward_q8(abi, T, ax, z, ys, xs, q, *scratch(px.poetx_forward_q8_workspace_bytes(abi, T, q)))
+        nb = px.poetx_backward_q8_workspace_bytes(abi, T, int(ys is not None), q)
+        dqR, dqP = out(m // b, tri, dtype=F32), out(n // b, tri, dtype=F32)
+        px.poetx_backward_q8(abi, T, ax, ys, xs, q, adz, dx, dqR, dqP, 0, *scratch(nb))
+        dGR, dGP = out(m // b, b, b, dtype=F32), out(n // b, b, b, dtype=F32)
+        px.poetx_backward_dG_q8(abi, T, ax, ys, xs, q, adz, None, dGR, dGP, 0, *scratch(nb))
+        kept = [t for t in (ys, xs, *yc, *xc) if t is not None]
+        return [z, dx, dqR, dqP, dGR, dGP] + kept
+
+    for y in (None, "full", "codes"):
+        for xg in (None, "full", "codes"):
+            A = Around(0xff)
+            got, want = run(A, True, y, xg), run(None, False, y, xg)
+            assert all(torch.equal(a, w) for a, w in zip(got, want)), (y, xg)
+            assert A.untouched(), (y, xg)
