@@ -229,7 +229,7 @@ int dg_splits(int nblk, int b, int64_t T, int32_t dtype) {
 // each, and the eighth would be left without any; its part of the sum would be
 // what the accumulator held before).
 int gemm_splits(int splits, int64_t T, int32_t dtype) {
-  if (!use_tc(dtype)) return splits;  // (FFMA: a split without tokens is zeros)
+  if (!use_tc(dtype) || T <= 0) return splits;  // (FFMA: a split without tokens is zeros)
   const int64_t steps = (T + 63) / 64, each = (steps + splits - 1) / splits;
   return static_cast<int>((steps + each - 1) / each);
 }

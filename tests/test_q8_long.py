@@ -48,6 +48,17 @@ def test_partial_sums_for_every_2048_tokens(b, T):
     assert more >= expanded + 2 * sums
 
 
+@pytest.mark.parametrize("dtype", [px.POETX_BF16, px.POETX_FP32])
+@pytest.mark.parametrize("b", [64, 128, 256, 512])
+def test_sizes_of_few_tokens(b, dtype):
+    pbuild.build()
+    L = px.poetx_layer(1024, 512, b, dtype, 16, 16, 16, 16, 16, 16, 16, 0)
+    for T in (0, 1, 63, 64, 65, 129):
+        assert px.poetx_block_backward_workspace_bytes(T, 1024, b, dtype) >= 4 * 1024 * b
+        for q in (px.poetx_q8(), px.poetx_q8(16, 16, 16, 16, 16, 16)):
+            assert px.poetx_backward_q8_workspace_bytes(L, T, 0, q) >= 4 * (1024 + 512) * b
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,d", [(16384, 8192), (5000, 8192), (16384, 1024)])
 @pytest.mark.parametrize("b", [64, 128, 256, 512])
